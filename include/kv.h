@@ -408,6 +408,153 @@ int kv_set_camera_only(kv_cache_t* cache, int on);
 int kv_run_static(kv_cache_t* const* caches, int n_streams, int block, int tiles_per_split,
                   const void* q, void* out, int check, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Token operators: what a program needs that answers one token at a time from
+ * paged pools of the same layout, [max_pages, 2 (K/V), page_size, H, D].
+ *
+ * Rotary positions. Pair i of a head's first rot_dim values at position p
+ * turns by the angle p * theta_i:
+ *     (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * theta_i = base^(-2i / rot_dim), scaled for contexts longer than the trained
+ * one by one of
+ *   KV_ROPE_LINEAR  theta_i / factor (positions interpolated)
+ *   KV_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   KV_ROPE_YARN    theta_i (g + (1 - g) / factor), g = the share, clamped to
+ *                   [0, 1], at which the pair's turns over original_context,
+ *                   original_context * theta_i / 2 pi, lie between low_turns
+ *                   and high_turns; amplitude 0.1 ln(factor) + 1
+ * (Peng et al., "YaRN: Efficient Context Window Extension of Large Language
+ * Models".) Angles are reduced modulo a turn without loss, to within 2^-30 of
+ * a turn, for every 32-bit position, negative ones included. Frequencies are
+ * at most 64 radians a position.
+ *
+ * Paged sequences. Token j of sequence s is row j % page_size of page
+ * tables[s][j / page_size]. Tables and lengths are device arrays that the
+ * kernels read when they run, so a captured call serves growing sequences.
+ * A table entry outside [0, max_pages), or a length outside
+ * [0, table_width * page_size], raises a bit of the error word
+ * (kv_tokens_check); such tokens are neither written nor attended to, and
+ * lengths are held to that range. Table entries past a sequence's last page
+ * are not read. Length 0 marks an unused row of the batch.
+ *
+ * All calls: device pointers belong to the caller and lie on the current
+ * device, to which `stream` belongs. Calls do not synchronise and can be
+ * captured. Inputs must not overlap outputs except where a call says so.
+ * Sizes of zero are allowed and launch nothing.
+ */
+
+/* kv_rotate also takes 32-bit tensors. */
+enum { KV_FP32 = 2 };
+
+/* Pairs: (i, i + rot_dim / 2), or neighbours (2i, 2i + 1). */
+enum { KV_ROPE_HALF = 0, KV_ROPE_INTERLEAVED = 1 };
+
+enum { KV_ROPE_NONE = 0, KV_ROPE_LINEAR = 1, KV_ROPE_NTK = 2, KV_ROPE_YARN = 3 };
+
+/* Bounds on a call: sequences, query heads, head_dim of kv_rotate. */
+#define KV_MAX_TOKEN_SEQS 16384
+#define KV_MAX_Q_HEADS 8192
+#define KV_MAX_ROTATE_DIM 512
+
+typedef struct kv_rope kv_rope_t; /* frequencies of a rotation; host state */
+
+/* Rows [n, heads, head_dim] of a device tensor: head h of token t starts at
+ * element t * token_stride + h * head_stride, its values next to each other. */
+typedef struct kv_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kv_rows;
+
+/* A batch of paged sequences; every pointer is borrowed. */
+typedef struct kv_tokens {
+  void* pool;             /* [max_pages, 2, page_size, num_heads, head_dim], 16-byte aligned */
+  const int32_t* tables;  /* [n_seqs] rows of table_width page ids, table_stride apart */
+  const int32_t* lens;    /* [n_seqs] tokens of each sequence, the new ones included */
+  uint32_t* error;        /* device error word, zeroed by the caller once */
+  int64_t table_stride;
+  int max_pages, page_size, num_heads, head_dim, dtype;
+  int table_width, n_seqs;
+} kv_tokens;
+
+/* kv_rope_init -- a rotation of the first rot_dim values of a head (even, 2 to
+ * 256). factor, original_context, low_turns and high_turns count only for the
+ * scalings that use them; amplitude 0 is the scaling's own (1 but for
+ * KV_ROPE_YARN with factor > 1). Errors: KV_ERR_ARG. No CUDA call is made; the handle
+ * serves every device and is released with kv_rope_free. */
+int kv_rope_init(kv_rope_t** out, int rot_dim, int layout, int scaling, double base, double factor,
+                 double original_context, double low_turns, double high_turns, double amplitude);
+
+/* kv_rope_init_frequencies -- the same with rot_dim / 2 frequencies given in
+ * radians a position (any other scaling), |theta| <= 64. */
+int kv_rope_init_frequencies(kv_rope_t** out, int rot_dim, int layout, const double* theta, double amplitude);
+
+/* kv_rope_free -- NULL is ignored. */
+void kv_rope_free(kv_rope_t* rope);
+
+/* kv_rope_get -- what the handle holds; up to `cap` frequencies into theta. */
+int kv_rope_get(const kv_rope_t* rope, int* rot_dim, int* layout, double* amplitude, double* theta, int cap);
+
+/* kv_rotate -- rotate x [n_tokens, n_heads, head_dim] at positions [n_tokens]
+ * (int32) into out; values behind rot_dim are copied. inverse != 0 turns by
+ * the negative angle with the same amplitude, which is the gradient of the
+ * call without it. out may be x itself (same address and strides). KV_BF16,
+ * KV_FP16 or KV_FP32; the sums are in 32 bits, rounded once. head_dim even,
+ * at most KV_MAX_ROTATE_DIM.
+ * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CUDA. */
+int kv_rotate(const kv_rope_t* rope, const kv_rows* x, const kv_rows* out, const int32_t* positions, int n_tokens,
+              int n_heads, int head_dim, int dtype, int inverse, void* stream);
+
+/* kv_append_tokens -- write new tokens' k and v [n_tokens, H, D] to the pool,
+ * the keys rotated on the way (rope NULL: as they are). cu_new [n_seqs + 1]
+ * (device, starting at 0, not decreasing): tokens [cu_new[s], cu_new[s + 1])
+ * are the last tokens of sequence s, whose lens[s] counts them already; tokens
+ * behind cu_new[n_seqs] are padding and are not written, nor are those of a
+ * sequence of length 0. cu_new NULL: one new token per sequence. positions
+ * [n_tokens] are the angles' positions (NULL: the token's index in its
+ * sequence). No two new tokens of a call may share a slot. Rows of k and v
+ * start on 16-byte boundaries.
+ * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED (head_dim must be 64 or 128),
+ * KV_ERR_CUDA. A cu_new that runs backwards, or gives a sequence more tokens
+ * than its length, raises the error word, and those tokens are not written. */
+int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int n_tokens, const int32_t* cu_new,
+                     const kv_rope_t* rope, const int32_t* positions, void* stream);
+
+/* kv_decode_workspace_bytes -- device workspace of kv_decode and
+ * kv_decode_append; depends on head_dim, the heads and the current device
+ * only. 0 on bad input. */
+size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads);
+
+/* kv_decode -- attention of one new token per sequence: for sequence s and
+ * query head i, with K/V head i / (q_heads / H),
+ *     out[s, i] = sum_j softmax_j(scale q[s, i] . k_j) v_j
+ * over its tokens j in [max(0, lens[s] - window), lens[s]) (window 0: all of
+ * them). q [n_seqs, q_heads, D], rows on 16-byte boundaries; out
+ * [n_seqs, q_heads, D] contiguous, in the pool's dtype. scale 0 is 1/sqrt(D).
+ * Rows of length 0 give zeros. fp32 statistics and sums, rounded once; equal
+ * inputs give equal bits. workspace (kv_decode_workspace_bytes, 16-byte
+ * aligned) needs no initial value and keeps nothing between calls; calls that
+ * may overlap on the GPU need one each.
+ * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY (workspace),
+ * KV_ERR_CUDA. */
+int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, int window, void* out, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/* kv_decode_append -- a decode step: kv_append_tokens of one token per
+ * sequence, the rotation of q at the same position, and kv_decode, without
+ * the launches and passes between them. k, v [n_seqs, H, D]; positions
+ * [n_seqs] or NULL (lens[s] - 1). The new key counts in the pool's dtype, as
+ * later steps read it; the rotated query is not rounded. A page that the
+ * sequence's new token is written to must not be another sequence's as well.
+ * Errors: as kv_decode. */
+int kv_decode_append(const kv_tokens* c, const kv_rows* k, const kv_rows* v, const kv_rows* q, int q_heads,
+                     const kv_rope_t* rope, const int32_t* positions, float scale, int window, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* kv_tokens_check -- synchronise `stream` and read the error word; a raised
+ * one is cleared. KV_OK, KV_ERR_DEVICE_CHECK or KV_ERR_CUDA. */
+int kv_tokens_check(const kv_tokens* c, void* stream);
+
 /* kv_testing_fail_launches -- for tests of the error paths only: the next n
  * kernel launches the library makes (any call, any thread) return
  * cudaErrorLaunchFailure, and so KV_ERR_CUDA, without launching anything.

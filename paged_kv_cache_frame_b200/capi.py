@@ -24,7 +24,17 @@ KV_ERR_UNSUPPORTED = -9
 KV_ERR_STALE_PLAN = -10
 KV_BF16 = 0
 KV_FP16 = 1
+KV_FP32 = 2
+KV_ROPE_HALF = 0
+KV_ROPE_INTERLEAVED = 1
+KV_ROPE_NONE = 0
+KV_ROPE_LINEAR = 1
+KV_ROPE_NTK = 2
+KV_ROPE_YARN = 3
 KV_MAX_STREAMS = 32
+KV_MAX_TOKEN_SEQS = 16384
+KV_MAX_Q_HEADS = 8192
+KV_MAX_ROTATE_DIM = 512
 KV_STATIC_SCRATCH_BYTES = 32 << 20
 KV_NOT_CURRENT = -0x40000000   # krow of a tile that is not the open step's frame
 
@@ -57,6 +67,18 @@ class kv_plan_stats(ctypes.Structure):
                 ("upload_launches", ctypes.c_int)]
 
 
+class kv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class kv_tokens(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("error", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("table_width", ctypes.c_int),
+                ("n_seqs", ctypes.c_int)]
+
+
 class KVError(RuntimeError):
     def __init__(self, code: int, where: str, detail: str):
         self.code = code
@@ -68,6 +90,11 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _IP = ctypes.POINTER(ctypes.c_int)
+_D = ctypes.c_double
+_DP = ctypes.POINTER(ctypes.c_double)
+_F = ctypes.c_float
+_ROWS = ctypes.POINTER(kv_rows)
+_TOKENS = ctypes.POINTER(kv_tokens)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -98,6 +125,16 @@ SIGNATURES = {
     "kv_run_static": (_I, [ctypes.POINTER(_P), _I, _I, _I, _P, _P, _I, _P]),
     "kv_set_cross_frame_special": (_I, [_P, _I]),
     "kv_set_camera_only": (_I, [_P, _I]),
+    "kv_rope_init": (_I, [ctypes.POINTER(_P), _I, _I, _I, _D, _D, _D, _D, _D, _D]),
+    "kv_rope_init_frequencies": (_I, [ctypes.POINTER(_P), _I, _I, _DP, _D]),
+    "kv_rope_free": (None, [_P]),
+    "kv_rope_get": (_I, [_P, _IP, _IP, _DP, _DP, _I]),
+    "kv_rotate": (_I, [_P, _ROWS, _ROWS, _P, _I, _I, _I, _I, _I, _P]),
+    "kv_append_tokens": (_I, [_TOKENS, _ROWS, _ROWS, _I, _P, _P, _P, _P]),
+    "kv_decode_workspace_bytes": (_SZ, [_TOKENS, _I]),
+    "kv_decode": (_I, [_TOKENS, _ROWS, _I, _F, _I, _P, _P, _SZ, _P]),
+    "kv_decode_append": (_I, [_TOKENS, _ROWS, _ROWS, _ROWS, _I, _P, _P, _F, _I, _P, _P, _SZ, _P]),
+    "kv_tokens_check": (_I, [_TOKENS, _P]),
     "kv_testing_fail_launches": (None, [_I]),
     "kv_strerror": (ctypes.c_char_p, [_I]),
     "kv_last_error": (ctypes.c_char_p, []),

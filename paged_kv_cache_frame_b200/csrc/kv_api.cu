@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/kv.h"
+#include "api_error.h"
 #include "kernels.h"
 #include "kv_state.h"
 #include "launch.cuh"
@@ -98,6 +99,9 @@ int device_sms() {
 
 namespace pkv {
 std::atomic<int> g_fail_launches{0};
+int api_fail(int code, const std::string& why) { return fail(code, why); }
+int api_cuda_fail(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+int current_device_sms() { return device_sms(); }
 }
 
 extern "C" {

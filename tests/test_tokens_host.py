@@ -1,0 +1,324 @@
+"""Token operators on the host: refusals, frequencies, and models of the index
+arithmetic that the kernels use. No GPU, no launches."""
+import ctypes
+import math
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(HERE, "..", "paged_kv_cache_frame_b200", "csrc")
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_cache_frame_b200 import build
+    build.build()
+    import paged_kv_cache_frame_b200 as m
+    return m
+
+
+def code(pkv, f, *args):
+    with pytest.raises(pkv.KVError) as e:
+        f(*args)
+    return e.value.name
+
+
+# ---------------------------------------------------------------- frequencies
+def theta(rot, base, scaling, factor=1.0, context=0.0, low=1.0, high=32.0):
+    out = []
+    for i in range(rot // 2):
+        t = base ** (-2 * i / rot)
+        if scaling == "linear":
+            t = t / factor
+        if scaling == "ntk":
+            # another base, such that the last pair turns `factor` times slower
+            t = (base * factor ** (rot / (rot - 2))) ** (-2 * i / rot) if rot > 2 else t
+        if scaling == "yarn":
+            turns = context * t / (2 * math.pi)
+            g = min(1.0, max(0.0, (turns - low) / (high - low)))
+            t = (1 - g) * t / factor + g * t
+        out.append(t)
+    return out
+
+
+@pytest.mark.parametrize("rot,scaling,kw", [
+    (128, "none", {}), (2, "none", {}), (2, "ntk", {"factor": 8.0}), (64, "linear", {"factor": 2.5}),
+    (256, "ntk", {"factor": 16.0}), (96, "yarn", {"factor": 4.0, "context": 4096}),
+    (48, "yarn", {"factor": 8.0, "context": 1024, "low": 1.0, "high": 4.0})])
+def test_frequencies(pkv, rot, scaling, kw):
+    r = pkv.Rope(rot, base=5e5, scaling=scaling, factor=kw.get("factor", 1.0), original_context=kw.get("context", 0),
+                 low_turns=kw.get("low", 1.0), high_turns=kw.get("high", 32.0))
+    assert r.inv_freq == pytest.approx(theta(rot, 5e5, scaling, **kw), rel=1e-14)
+    assert r.amplitude == pytest.approx(0.1 * math.log(kw["factor"]) + 1 if scaling == "yarn" else 1.0, rel=1e-15)
+
+
+def test_given_frequencies_and_amplitude(pkv):
+    r = pkv.Rope(6, layout="interleaved", inv_freq=[1.0, -0.25, 7.5], amplitude=1.25)
+    assert (r.inv_freq, r.amplitude, r.rot_dim, r.layout) == ([1.0, -0.25, 7.5], 1.25, 6, "interleaved")
+    assert pkv.Rope(8, scaling="yarn", factor=4.0, original_context=64, amplitude=1.0).amplitude == 1.0
+
+
+@pytest.mark.parametrize("kw", [
+    {"rot_dim": 0}, {"rot_dim": 3}, {"rot_dim": 258}, {"rot_dim": 64, "base": 0.0}, {"rot_dim": 64, "base": math.nan},
+    {"rot_dim": 64, "scaling": "linear", "factor": 0.0}, {"rot_dim": 64, "scaling": "yarn", "factor": 2.0},
+    {"rot_dim": 64, "scaling": "yarn", "factor": 2.0, "original_context": 64, "low_turns": 4.0, "high_turns": 4.0},
+    {"rot_dim": 4, "inv_freq": [1.0, math.inf]}, {"rot_dim": 4, "inv_freq": [1.0, 2e6]},
+    {"rot_dim": 4, "inv_freq": [1.0, 0.5], "amplitude": math.inf}])
+def test_rope_refusals(pkv, kw):
+    assert code(pkv, lambda: pkv.Rope(**kw)) == "ARG"
+
+
+@pytest.mark.parametrize("kw", [
+    {"rot_dim": 4, "layout": "thirds"}, {"rot_dim": 4, "scaling": "cubic"}, {"rot_dim": 4, "amplitude": 0.0},
+    {"rot_dim": 4, "amplitude": math.nan}, {"rot_dim": 4, "inv_freq": [1.0]},
+    {"rot_dim": 2, "inv_freq": [1.0], "scaling": "ntk", "factor": 2.0}])
+def test_rope_argument_errors(pkv, kw):
+    with pytest.raises(ValueError):
+        pkv.Rope(**kw)
+
+
+def test_rope_c_refusals(pkv):
+    L = pkv.capi.lib()
+    d = (ctypes.c_double * 1)(1.0)
+    assert L.kv_rope_init_frequencies(None, 2, 0, d, 1.0) == pkv.capi.KV_ERR_ARG
+    h = ctypes.c_void_p()
+    assert L.kv_rope_init_frequencies(ctypes.byref(h), 2, 0, None, 1.0) == pkv.capi.KV_ERR_ARG
+    assert L.kv_rope_init_frequencies(ctypes.byref(h), 2, 5, d, 1.0) == pkv.capi.KV_ERR_ARG
+    assert h.value is None
+    L.kv_rope_free(None)
+    assert L.kv_rope_get(None, None, None, None, None, 0) == pkv.capi.KV_ERR_ARG
+
+
+# ---------------------------------------------------------------- refusals before any launch
+def rows(pkv, at=4096, token=128, head=64):
+    return pkv.capi.kv_rows(at, token, head)
+
+
+def tokens(pkv, **kw):
+    """A batch whose addresses are never followed: every call here is refused
+    or has nothing to do."""
+    f = dict(pool=4096, tables=4096, lens=4096, error=4096, table_stride=4, max_pages=8, page_size=16, num_heads=2,
+             head_dim=64, dtype=pkv.KV_BF16, table_width=4, n_seqs=3)
+    f.update(kw)
+    return pkv.capi.kv_tokens(**f)
+
+
+BAD_TOKENS = [
+    ({"head_dim": 96}, "UNSUPPORTED"), ({"dtype": 2}, "UNSUPPORTED"), ({"dtype": -1}, "UNSUPPORTED"),
+    ({"max_pages": 0}, "ARG"), ({"page_size": 0}, "ARG"), ({"num_heads": 0}, "ARG"), ({"num_heads": 9000}, "ARG"),
+    ({"n_seqs": -1}, "ARG"), ({"n_seqs": 16385}, "ARG"), ({"table_width": 0}, "ARG"), ({"table_stride": 3}, "ARG"),
+    ({"pool": None}, "ARG"), ({"pool": 4104}, "ARG"), ({"tables": None}, "ARG"), ({"lens": None}, "ARG"),
+    ({"error": None}, "ARG"), ({"error": 4098}, "ARG"), ({"tables": 4097}, "ARG"),
+    ({"table_width": 1 << 20, "table_stride": 1 << 20, "page_size": 4096}, "ARG"),
+    ({"max_pages": 1 << 20, "page_size": 1024}, "ARG")]
+
+
+@pytest.mark.parametrize("kw,want", BAD_TOKENS, ids=lambda x: str(x))
+def test_sequence_refusals(pkv, kw, want):
+    c, r = tokens(pkv, **kw), rows(pkv)
+    assert code(pkv, pkv.kv_append_tokens, c, r, r, 3) == want
+    assert code(pkv, pkv.kv_decode, c, r, 2, 0.0, 0, 4096, 4096, 1 << 30) == want
+    assert code(pkv, pkv.kv_decode_append, c, r, r, r, 2, None, None, 0.0, 0, 4096, 4096, 1 << 30) == want
+    assert pkv.kv_decode_workspace_bytes(c, 2) == 0
+
+
+def test_append_refusals(pkv):
+    c, r = tokens(pkv), rows(pkv)
+    wide = pkv.Rope(128)
+    for args in [(None, r, r, 3), (c, r, r, -1), (c, r, r, 4), (c, None, r, 3), (c, r, None, 3),
+                 (c, rows(pkv, at=None), r, 3), (c, rows(pkv, at=4100), r, 3), (c, r, rows(pkv, token=132), 3),
+                 (c, r, rows(pkv, head=68), 3), (c, r, r, 3, 4098), (c, r, r, 3, None, None, 4098),
+                 (c, r, r, 3, None, wide.handle)]:
+        assert code(pkv, pkv.kv_append_tokens, *args) == "ARG"
+
+
+def test_decode_refusals(pkv):
+    c, r = tokens(pkv), rows(pkv)
+    wide, big = pkv.Rope(128), 1 << 30
+    need = pkv.kv_decode_workspace_bytes(c, 2)
+    assert need > 0
+    assert code(pkv, pkv.kv_decode, c, r, 2, 0.0, 0, 4096, 4096, need - 1) == "CAPACITY"
+    for args in [(None, r, 2, 0.0, 0, 4096, 4096, big), (c, None, 2, 0.0, 0, 4096, 4096, big),
+                 (c, r, 0, 0.0, 0, 4096, 4096, big), (c, r, 3, 0.0, 0, 4096, 4096, big),
+                 (c, r, 8194, 0.0, 0, 4096, 4096, big), (c, r, 2, math.inf, 0, 4096, 4096, big),
+                 (c, r, 2, math.nan, 0, 4096, 4096, big), (c, r, 2, 0.0, -1, 4096, 4096, big),
+                 (c, r, 2, 0.0, 0, None, 4096, big), (c, r, 2, 0.0, 0, 4098, 4096, big),
+                 (c, r, 2, 0.0, 0, 4096, None, big), (c, r, 2, 0.0, 0, 4096, 4104, big),
+                 (c, rows(pkv, at=4098), 2, 0.0, 0, 4096, 4096, big), (c, rows(pkv, head=66), 2, 0.0, 0, 4096, 4096, big)]:
+        assert code(pkv, pkv.kv_decode, *args) == "ARG"
+    for k, v, rope, pos in [(None, r, None, None), (r, None, None, None), (r, r, wide.handle, None),
+                            (r, r, None, 4098), (rows(pkv, at=4104), r, None, None)]:
+        assert code(pkv, pkv.kv_decode_append, c, k, v, r, 2, rope, pos, 0.0, 0, 4096, 4096, big) == "ARG"
+    assert code(pkv, pkv.kv_tokens_check, None) == "ARG"
+    assert pkv.kv_decode_workspace_bytes(c, 3) == 0
+
+
+def test_rotate_refusals(pkv):
+    r, x = pkv.Rope(64), rows(pkv)
+    for args, want in [((None, x, x, 4096, 3, 2, 64, 0), "ARG"), ((r.handle, None, x, 4096, 3, 2, 64, 0), "ARG"),
+                       ((r.handle, x, None, 4096, 3, 2, 64, 0), "ARG"), ((r.handle, x, x, None, 3, 2, 64, 0), "ARG"),
+                       ((r.handle, x, x, 4098, 3, 2, 64, 0), "ARG"), ((r.handle, x, x, 4096, -1, 2, 64, 0), "ARG"),
+                       ((r.handle, x, x, 4096, 3, -1, 64, 0), "ARG"), ((r.handle, x, x, 4096, 3, 2, 62, 0), "ARG"),
+                       ((r.handle, x, x, 4096, 3, 2, 65, 0), "ARG"), ((r.handle, x, x, 4096, 3, 2, 514, 0), "ARG"),
+                       ((r.handle, rows(pkv, at=4097), x, 4096, 3, 2, 64, 0), "ARG"),
+                       ((r.handle, x, rows(pkv, at=4098), 4096, 3, 2, 64, 2), "ARG"),
+                       ((r.handle, x, rows(pkv, token=256), 4096, 3, 2, 64, 0), "ARG"),
+                       ((r.handle, x, x, 4096, 3, 2, 64, 3), "UNSUPPORTED")]:
+        assert code(pkv, pkv.kv_rotate, *args) == want
+
+
+def test_nothing_to_do_launches_nothing(pkv):
+    r, x = pkv.Rope(64), rows(pkv)
+    nul = rows(pkv, at=None)
+    pkv.kv_testing_fail_launches(1)   # a launch would take this one and fail
+    try:
+        pkv.kv_rotate(r.handle, nul, nul, None, 0, 2, 64, 0)
+        pkv.kv_rotate(r.handle, nul, nul, None, 3, 0, 64, 0)
+        pkv.kv_append_tokens(tokens(pkv), nul, nul, 0, 4096)
+        c = tokens(pkv, n_seqs=0, tables=None, lens=None)
+        pkv.kv_append_tokens(c, nul, nul, 0)
+        pkv.kv_decode(c, nul, 2, 0.0, 0, None, None, 0)
+        pkv.kv_decode_append(c, nul, nul, nul, 2, r.handle, None, 0.0, 0, None, None, 0)
+        assert code(pkv, pkv.kv_append_tokens, tokens(pkv), x, x, 3) == "CUDA"
+    finally:
+        pkv.kv_testing_fail_launches(0)
+
+
+def test_failing_launches_are_reported(pkv):
+    c, r, x = tokens(pkv), pkv.Rope(64), rows(pkv)
+    big = 1 << 30
+    for call in [lambda: pkv.kv_rotate(r.handle, x, x, 4096, 3, 2, 64, 0),
+                 lambda: pkv.kv_append_tokens(c, x, x, 3, None, r.handle),
+                 lambda: pkv.kv_append_tokens(c, x, x, 7, 4096, r.handle)]:
+        pkv.kv_testing_fail_launches(1)
+        try:
+            assert code(pkv, call) == "CUDA"
+        finally:
+            pkv.kv_testing_fail_launches(0)
+
+
+def test_tensors_are_checked_before_the_call(pkv):
+    import torch
+    r = pkv.Rope(64)
+    x, pos = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for a, p in [(x, pos), (x[0], pos), (x.double(), pos), (x, pos.long()), (x, pos[:2]),
+                 (x.transpose(1, 2), pos), (x.permute(2, 1, 0), pos)]:
+        with pytest.raises(ValueError):
+            r.rotate(a, p)
+    with pytest.raises(ValueError):
+        r.rotate(x.float().requires_grad_(), pos, out=torch.empty(3, 2, 64))
+    with pytest.raises(ValueError):
+        pkv.PagedTokens(torch.zeros(4, 2, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32),
+                        torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        pkv.PagedTokens(torch.zeros(4, 3, 16, 2, 64, dtype=torch.bfloat16), None, None)
+    with pytest.raises(ValueError):
+        pkv.PagedTokens(torch.zeros(4, 2, 16, 2, 64), None, None)
+
+
+# ---------------------------------------------------------------- index arithmetic
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_page_divisor(tmp_path):
+    exe = tmp_path / "page_divisor"
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", CSRC, os.path.join(HERE, "cpp", "page_divisor.cpp"),
+                    "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
+
+
+def find_seq(cu, n, t):
+    """The kernel's search: 32 probes a round."""
+    lo, hi, reads = 0, n, []
+    while lo < hi:
+        step = (hi - lo + 31) // 32
+        k = 0
+        for lane in range(32):
+            probe = lo + (lane + 1) * step - 1
+            if probe < hi:
+                reads.append(probe + 1)
+                k += cu[probe + 1] <= t
+        lo = min(lo + k * step, hi)
+        hi = min(lo + step - 1, hi)
+    assert all(0 < i <= n for i in reads)
+    return lo
+
+
+def test_sequence_search():
+    rng = random.Random(5)
+    for n in (1, 2, 31, 32, 33, 64, 100, 1000, 1024, 1025, 5000):
+        cu = [0]
+        for _ in range(n):
+            cu.append(cu[-1] + rng.choice([0, 0, 1, 3]))
+        for t in sorted({0, cu[-1] - 1, cu[-1], cu[-1] + 5, *(rng.randrange(cu[-1] + 1) for _ in range(60))}):
+            if t >= 0:
+                assert find_seq(cu, n, t) == sum(c <= t for c in cu[1:])
+    # out of order: any answer in range will do, the search ends and reads in range
+    for _ in range(300):
+        n = rng.randint(1, 3000)
+        cu = [rng.randint(-5, 50) for _ in range(n + 1)]
+        assert 0 <= find_seq(cu, n, rng.randint(0, 50)) <= n
+
+
+def line_parts(tiles, units, grid):
+    """(unit key, CTA, slot, first tile, last tile) of every piece, as the
+    attention kernel cuts the line, and the parts its last pieces announce."""
+    total = sum(t * units for t in tiles)
+    parts = min(grid, total)
+    pieces, meta = [], {}
+    for c in range(parts):
+        t, end = c * total // parts, (c + 1) * total // parts
+        base, seq = 0, 0
+        while not (tiles[seq] * units and base <= t < base + tiles[seq] * units):
+            base += tiles[seq] * units
+            seq += 1
+        meta[c] = 0
+        while t < end:
+            n = tiles[seq]
+            unit, t0 = divmod(t - base, n)
+            t1 = n if n - t0 < end - t else t0 + end - t
+            whole = t0 == 0 and t1 == n
+            opens = t0 == 0 and not whole
+            pieces.append(((seq, unit), c, None if whole else 2 * c + (1 if opens else 0), t0, t1))
+            if opens:
+                last = base + (unit + 1) * n - 1
+                meta[c] = ((last + 1) * parts - 1) // total - c + 1
+            t += t1 - t0
+            if t >= base + n * units and t < end:
+                base += n * units
+                seq += 1
+                while tiles[seq] == 0:
+                    seq += 1
+    return pieces, meta
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_split_covers_every_tile_and_the_join_finds_the_parts(seed):
+    rng = random.Random(seed)
+    seqs, units, grid = rng.choice([1, 2, 7, 64, 300]), rng.choice([1, 2, 8, 24]), rng.choice([1, 4, 296])
+    tiles = [rng.choice([0, 1, 2, 5, rng.randint(0, 400)]) for _ in range(seqs)]
+    if not sum(tiles):
+        tiles[-1] = 1
+    pieces, meta = line_parts(tiles, units, grid)
+    by_unit, used = {}, set()
+    for key, c, slot, t0, t1 in pieces:
+        by_unit.setdefault(key, []).append((t0, t1, c, slot))
+        if slot is not None:
+            assert slot < 2 * grid and slot not in used
+            used.add(slot)
+    assert set(by_unit) == {(s, u) for s in range(seqs) if tiles[s] for u in range(units)}
+    joined = set()
+    for (seq, _), p in by_unit.items():
+        p.sort()
+        assert p[0][0] == 0 and p[-1][1] == tiles[seq] and all(a[1] == b[0] for a, b in zip(p, p[1:]))
+        if len(p) > 1:
+            c = p[0][2]
+            assert meta[c] == len(p)
+            assert [x[3] for x in p] == [2 * (c + i) + (1 if i == 0 else 0) for i in range(len(p))]
+            joined.add(c)
+        else:
+            assert p[0][3] is None
+    assert joined == {c for c, n in meta.items() if n}
