@@ -2,11 +2,12 @@
 // way, the values as they are, each row to the page and slot that the
 // sequence's table gives for the token's index.
 //
-// Bound by its bytes. As in the rotation kernel a thread keeps one unit of V
-// pairs of a token and goes through the heads with its angles; the values'
-// packs 2u and 2u + 1 travel in the same thread. A warp finds the sequence of
-// a token in cu_new with 32 probes at a time (two rounds for up to 1024
-// sequences), once per token of the block.
+// Bound by its bytes. As in the rotation kernel a block takes a few tokens
+// with all of their heads, and its threads go through the (token, head) rows,
+// each at its own unit of V pairs; the values' packs 2u and 2u + 1 travel in
+// the same thread. A warp finds the sequence of a token in cu_new with 32
+// probes at a time (two rounds for up to 1024 sequences) while the first rows
+// are on their way.
 #include "launch.cuh"
 #include "rope_unit.cuh"
 
@@ -14,8 +15,8 @@ namespace pkv {
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;         // heads in flight per thread, keys and values
-constexpr int kMaxTokens = 64;    // tokens a block takes
+constexpr int kAhead = 2;         // rows in flight per thread, keys and values
+constexpr int kMaxTokens = 16;    // tokens of a block
 
 // Sequences s of [0, n) with cu[s + 1] <= t, all before the others: the
 // sequence of token t (n where no sequence holds it). All lanes of a warp.
@@ -35,19 +36,40 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
 }  // namespace
 
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads) append_tokens_kernel(const __grid_constant__ AppendTokensArgs a, int units,
-                                                                 int head_slots) {
+__global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid_constant__ AppendTokensArgs a, int units,
+                                                                 int per_block) {
+  extern __shared__ __align__(16) float2 s_angle[];
   __shared__ int s_row[kMaxTokens];   // pool row of the token's key, -1: not written
-  __shared__ int s_pos[kMaxTokens];
   const int u = threadIdx.x % units;
-  const int row = threadIdx.x / units;
-  const int per_block = min(kMaxTokens, kThreads / units / head_slots);
+  const int slot = threadIdx.x / units, slots = kThreads / units;
   const int first = (int)blockIdx.x * per_block;
+  const int tokens = min(per_block, a.n_tokens - first);
+  const int rows = tokens * a.c.H;
+  const RopeUnit<T, V, kInter> unit(u, a.c.D, a.rope.rot);
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x / 32; i < per_block; i += kThreads / 32) {
+  using P = Pack<T, V>;
+  P k0[kAhead], k1[kAhead], v0[kAhead], v1[kAhead];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * slots;
+      if (slot < slots && r < rows) {
+        const int t = divided(r, a.head_mul, a.head_shift), h = r - t * a.c.H;
+        const T* k = static_cast<const T*>(a.k.p) + (first + t) * a.k.token_stride + h * a.k.head_stride;
+        const T* v = static_cast<const T*>(a.v.p) + (first + t) * a.v.token_stride + h * a.v.head_stride;
+        k0[i] = *reinterpret_cast<const P*>(k + unit.at0);
+        k1[i] = *reinterpret_cast<const P*>(k + unit.at1);
+        v0[i] = *reinterpret_cast<const P*>(v + 2 * u * V);
+        v1[i] = *reinterpret_cast<const P*>(v + 2 * u * V + V);
+      }
+    }
+  };
+  load(slot);   // on their way while places and angles are worked out
+  // A warp a token: its row, then its angles.
+  const int lane = threadIdx.x % 32;
+  for (int i = threadIdx.x / 32; i < tokens; i += kThreads / 32) {
     const int t = first + i;
-    if (t >= a.n_tokens) break;
     int s = t, back = 1;   // the token is the back-th from the end of sequence s
     if (a.cu_new) {
       s = find_seq(a.cu_new, a.c.n_seqs, t);
@@ -57,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(const __grid_co
         back = __ldg(a.cu_new + s + 1) - t;
         if (t < __ldg(a.cu_new + s) || back < 1) {
           s = a.c.n_seqs;
-          if (threadIdx.x % 32 == 0) raise_error(a.c.error);
+          if (lane == 0) raise_error(a.c.error);
         }
       }
     }
@@ -74,72 +96,47 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(const __grid_co
       }
       if (bad) {
         at = -1;
-        if (threadIdx.x % 32 == 0) raise_error(a.c.error);
+        if (lane == 0) raise_error(a.c.error);
       }
       pos = a.positions ? __ldg(a.positions + t) : j;
     }
-    if (threadIdx.x % 32 == 0) {
-      s_row[i] = at;
-      s_pos[i] = pos;
+    if (lane == 0) s_row[i] = at;
+    for (int p = lane; p < a.rope.rot / 2; p += 32) {
+      float c, sn;
+      rope_angle(a.rope.turn[p], pos, a.rope.amplitude, c, sn);
+      s_angle[angle_at<V>(units, i, p)] = make_float2(c, sn);
     }
   }
   __syncthreads();
-  const int i = row / head_slots;
-  const int t = first + i;
-  if (i >= per_block || t >= a.n_tokens || s_row[i] < 0) return;
-  RopeUnit<T, V, kInter> unit;
-  unit.place(u, a.c.D, a.rope.rot);
-  if (unit.turns) unit.angles(a.rope, u, s_pos[i], false);
-  const T* k = static_cast<const T*>(a.k.p) + t * a.k.token_stride;
-  const T* v = static_cast<const T*>(a.v.p) + t * a.v.token_stride;
-  T* to = static_cast<T*>(a.c.pool) + row_offset(a.c, s_row[i], 0);
   const long long v_off = (long long)a.c.page_size * a.c.H * a.c.D;
-  using P = Pack<T, V>;
-  for (int h = row % head_slots; h < a.c.H; h += kAhead * head_slots) {
-    P k0[kAhead], k1[kAhead], v0[kAhead], v1[kAhead];
+  for (int r0 = slot; r0 < rows; r0 += kAhead * slots) {
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
-      const int g = h + n * head_slots;
-      if (g < a.c.H) {
-        const T* kp = k + g * a.k.head_stride;
-        const T* vp = v + g * a.v.head_stride;
-        k0[n] = *reinterpret_cast<const P*>(kp + unit.at0);
-        k1[n] = *reinterpret_cast<const P*>(kp + unit.at1);
-        v0[n] = *reinterpret_cast<const P*>(vp + 2 * u * V);
-        v1[n] = *reinterpret_cast<const P*>(vp + 2 * u * V + V);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
-      const int g = h + n * head_slots;
-      if (g < a.c.H) {
-        if (unit.turns) {
-          P y0, y1;
-          unit.turn(k0[n], k1[n], u, a.rope.rot, y0, y1);
-          k0[n] = y0;
-          k1[n] = y1;
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * slots;
+      if (slot < slots && r < rows) {
+        const int t = divided(r, a.head_mul, a.head_shift), h = r - t * a.c.H;
+        const int row = s_row[t];
+        if (row >= 0) {
+          if (unit.turns) unit.turn(k0[i], k1[i], s_angle, units, t, a.rope.rot);
+          T* p = static_cast<T*>(a.c.pool) + row_offset(a.c, row, h);
+          *reinterpret_cast<P*>(p + unit.at0) = k0[i];
+          *reinterpret_cast<P*>(p + unit.at1) = k1[i];
+          *reinterpret_cast<P*>(p + v_off + 2 * u * V) = v0[i];
+          *reinterpret_cast<P*>(p + v_off + 2 * u * V + V) = v1[i];
         }
-        T* p = to + (long long)g * a.c.D;
-        *reinterpret_cast<P*>(p + unit.at0) = k0[n];
-        *reinterpret_cast<P*>(p + unit.at1) = k1[n];
-        *reinterpret_cast<P*>(p + v_off + 2 * u * V) = v0[n];
-        *reinterpret_cast<P*>(p + v_off + 2 * u * V + V) = v1[n];
       }
     }
+    load(r0 + kAhead * slots);
   }
 }
 
 template <typename T, int V, bool kInter>
 static cudaError_t launch(const AppendTokensArgs& a, cudaStream_t stream) {
   const int units = a.c.D / (2 * V);
-  const int rows = kThreads / units;
-  // As in the rotation: a token's heads over just enough threads to fill the
-  // GPU.
-  int slots = 1;
-  while (2 * slots <= rows && slots < a.c.H && (long long)a.n_tokens * units * slots < 148 * 1024) slots *= 2;
-  const int per_block = rows / slots < kMaxTokens ? rows / slots : kMaxTokens;
+  const int per_block = rope_tokens_per_block(a.n_tokens, a.c.H, units, kThreads, kMaxTokens);
   const int blocks = (a.n_tokens + per_block - 1) / per_block;
-  return launch_pdl(append_tokens_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads), 0, stream, a, units, slots);
+  return launch_pdl(append_tokens_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads),
+                    (size_t)per_block * units * V * sizeof(float2), stream, a, units, per_block);
 }
 
 template <typename T>

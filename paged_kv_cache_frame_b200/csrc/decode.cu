@@ -55,26 +55,6 @@ struct Shape {
   static constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
 };
 
-template <typename T>
-constexpr bool kIsFp16 = false;
-template <>
-constexpr bool kIsFp16<__half> = true;
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return kIsFp16<T> ? cvt_pack_f16(a, b) : cvt_pack_bf16(a, b);
-}
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t x);
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
-  return __half22float2(*reinterpret_cast<__half2*>(&x));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
-  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-
 // (a, b) as packed 16-bit values and the packed remainders.
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -566,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_cons
     const float f = ex2_approx(ml.x - top);
     sum = fmaf(f, ml.y, sum);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(f, x.v[e], acc[e]);
+    for (int e = 0; e < V; ++e) acc[e] = fmaf(f, x.get(e), acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];

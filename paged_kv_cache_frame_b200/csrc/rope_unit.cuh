@@ -3,21 +3,33 @@
 // (i, i + rot / 2) lie in the packs at uV and uV + rot / 2, and the units
 // behind the rotated part copy two packs each. Pairs at or past rot / 2 of
 // the neighbouring layout are copied too.
+//
+// A block works the angles of its tokens out once, a thread a pair, into
+// shared memory: every head of a token takes them from there.
 #pragma once
 #include "rope.cuh"
 #include "token_access.cuh"
 
 namespace pkv {
 
+// Angle table of a block: [tokens][units][V] (cos, sin), laid out so that
+// neighbouring units' 16 bytes lie next to each other.
+template <int V>
+__host__ __device__ constexpr int angle_at(int units, int token, int pair) {
+  return V == 1 ? token * units + pair
+                : token * units * V + (pair % V / 2 * units + pair / V) * 2 + pair % 2;
+}
+
 template <typename T, int V, bool kInter>
 struct RopeUnit {
+  using P = Pack<T, V>;
+  int u;
   int at0, at1;        // first value of each pack
   bool turns;          // any pair of the unit is rotated
   bool second;         // the second pack lies inside the head
-  float c[V], s[V];
 
-  // Unit u of a head of D values. No angle yet.
-  __device__ __forceinline__ void place(int u, int D, int rot) {
+  // Unit u of a head of D values.
+  __device__ __forceinline__ RopeUnit(int unit, int D, int rot) : u(unit) {
     if (kInter) {
       at0 = 2 * u * V;
       at1 = at0 + V;
@@ -30,47 +42,52 @@ struct RopeUnit {
     second = at1 < D;
   }
 
-  // The angles of a position, negated for the inverse.
-  __device__ __forceinline__ void angles(const RopeTable& t, int u, int32_t pos, bool inverse) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int p = u * V + i;
-      if (p < t.rot / 2) {
-        rope_angle(t.turn[p], pos, t.amplitude, c[i], s[i]);
-        if (inverse) s[i] = -s[i];
-      } else {
-        c[i] = 1.f;
-        s[i] = 0.f;
-      }
-    }
-  }
-
-  __device__ __forceinline__ void turn(const Pack<T, V>& x0, const Pack<T, V>& x1, int u, int rot, Pack<T, V>& y0,
-                                       Pack<T, V>& y1) const {
-    if (kInter) {
-      T x[2 * V], y[2 * V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = x0.v[i], x[V + i] = x1.v[i];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float a = to_f32(x[2 * i]), b = to_f32(x[2 * i + 1]);
-        rope_turn(a, b, c[i], s[i]);
-        const bool on = u * V + i < rot / 2;   // the others keep their bits
-        y[2 * i] = on ? from_f32<T>(a) : x[2 * i];
-        y[2 * i + 1] = on ? from_f32<T>(b) : x[2 * i + 1];
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) y0.v[i] = y[i], y1.v[i] = y[V + i];
+  // Rotates the packs by the angles of the block's token `token`.
+  __device__ __forceinline__ void turn(P& x0, P& x1, const float2* table, int units, int token, int rot) const {
+    float2 cs[V];
+    if constexpr (V == 1) {
+      cs[0] = table[angle_at<V>(units, token, u)];
     } else {
 #pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(table + angle_at<V>(units, token, u * V + i));
+        cs[i] = make_float2(x.x, x.y);
+        cs[i + 1] = make_float2(x.z, x.w);
+      }
+    }
+    if constexpr (V == 1) {
+      float a = x0.get(0), b = x1.get(0);
+      rope_turn(a, b, cs[0].x, cs[0].y);
+      x0.set(a);
+      x1.set(b);
+    } else if constexpr (kInter) {
+#pragma unroll
       for (int i = 0; i < V; ++i) {
-        float a = to_f32(x0.v[i]), b = to_f32(x1.v[i]);
-        rope_turn(a, b, c[i], s[i]);
-        y0.v[i] = from_f32<T>(a);
-        y1.v[i] = from_f32<T>(b);
+        P& x = i < V / 2 ? x0 : x1;
+        const int j = i % (V / 2);
+        float a = x.get(2 * j), b = x.get(2 * j + 1);
+        rope_turn(a, b, cs[i].x, cs[i].y);
+        if (u * V + i < rot / 2) x.set2(j, a, b);   // the others keep their bits
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        float a = x0.get(i), b = x1.get(i), c = x0.get(i + 1), d = x1.get(i + 1);
+        rope_turn(a, b, cs[i].x, cs[i].y);
+        rope_turn(c, d, cs[i + 1].x, cs[i + 1].y);
+        x0.set2(i / 2, a, c);
+        x1.set2(i / 2, b, d);
       }
     }
   }
 };
+
+// Tokens a block takes: enough heads per thread to hide the angles, as long
+// as every SM still gets two blocks.
+inline int rope_tokens_per_block(int n_tokens, int heads, int units, int threads, int most) {
+  int n = 1;
+  while (2 * n <= most && 2LL * n * heads * units <= 8LL * threads && n_tokens / (2 * n) >= 2 * 148) n *= 2;
+  return n;
+}
 
 }  // namespace pkv

@@ -2,76 +2,81 @@
 // becomes m (a cos - b sin, b cos + a sin) with the angle p * theta_i and the
 // amplitude m; the gradient is the same with the negative angle.
 //
-// Bound by its bytes (each value read and written once). A thread keeps one
-// unit of V pairs of a token, works its angles out once and goes through the
-// token's heads with them, four heads' loads in flight; the threads of a
-// block split heads and tokens. Sums of two products are in 32 bits, rounded
-// once to the tensor's type.
+// Bound by its bytes (each value read and written once). A block takes a few
+// tokens with all of their heads; its threads go through the (token, head)
+// rows with several rows' loads in flight, each thread at its own unit of V
+// pairs. Sums of two products are in 32 bits, rounded once to the tensor's
+// type.
 #include "launch.cuh"
 #include "rope_unit.cuh"
 
 namespace pkv {
 
+namespace {
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // heads in flight per thread
+constexpr int kAhead = 2;        // rows in flight per thread
+constexpr int kMaxTokens = 16;   // tokens of a block
+}  // namespace
 
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a, int units,
-                                                          int head_slots) {
+__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_constant__ RotateArgs a, int units,
+                                                          int per_block) {
+  extern __shared__ __align__(16) float2 s_angle[];
   const int u = threadIdx.x % units;
-  const int row = threadIdx.x / units;
-  const int per_block = kThreads / units / head_slots;   // tokens
-  const int token = (int)blockIdx.x * per_block + row / head_slots;
-  const int h0 = row % head_slots;
+  const int slot = threadIdx.x / units, slots = kThreads / units;
+  const int first = (int)blockIdx.x * per_block;
+  const int tokens = min(per_block, a.n_tokens - first);
+  const int rows = tokens * a.n_heads;
+  const RopeUnit<T, V, kInter> unit(u, a.head_dim, a.rope.rot);
+  const bool on = slot < slots && (unit.turns || a.copy_rest);
   pdl_wait();
   pdl_trigger();
-  if (row >= per_block * head_slots || token >= a.n_tokens) return;
-  RopeUnit<T, V, kInter> unit;
-  unit.place(u, a.head_dim, a.rope.rot);
-  if (!unit.turns && !a.copy_rest) return;
-  const T* x = static_cast<const T*>(a.x.p) + token * a.x.token_stride;
-  T* y = static_cast<T*>(a.out.p) + token * a.out.token_stride;
-  if (unit.turns) unit.angles(a.rope, u, __ldg(a.positions + token), a.inverse);
-  for (int h = h0; h < a.n_heads; h += kAhead * head_slots) {
-    Pack<T, V> x0[kAhead], x1[kAhead];
+  using P = Pack<T, V>;
+  P x0[kAhead], x1[kAhead];
+  auto load = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int g = h + i * head_slots;
-      if (g < a.n_heads) {
-        const T* p = x + g * a.x.head_stride;
-        x0[i] = *reinterpret_cast<const Pack<T, V>*>(p + unit.at0);
-        if (unit.second) x1[i] = *reinterpret_cast<const Pack<T, V>*>(p + unit.at1);
+      const int r = r0 + i * slots;
+      if (on && r < rows) {
+        const int t = divided(r, a.head_mul, a.head_shift);
+        const T* p = static_cast<const T*>(a.x.p) + (first + t) * a.x.token_stride + (r - t * a.n_heads) * a.x.head_stride;
+        x0[i] = *reinterpret_cast<const P*>(p + unit.at0);
+        if (unit.second) x1[i] = *reinterpret_cast<const P*>(p + unit.at1);
       }
     }
+  };
+  load(slot);   // on their way while the angles are worked out
+  const int pairs = a.rope.rot / 2;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int t = i / pairs, p = i - t * pairs;
+    float c, s;
+    rope_angle(a.rope.turn[p], __ldg(a.positions + first + t), a.rope.amplitude, c, s);
+    s_angle[angle_at<V>(units, t, p)] = make_float2(c, a.inverse ? -s : s);
+  }
+  __syncthreads();
+  for (int r0 = slot; r0 < rows; r0 += kAhead * slots) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int g = h + i * head_slots;
-      if (g < a.n_heads) {
-        T* p = y + g * a.out.head_stride;
-        if (unit.turns) {
-          Pack<T, V> y0, y1;
-          unit.turn(x0[i], x1[i], u, a.rope.rot, y0, y1);
-          x0[i] = y0;
-          x1[i] = y1;
-        }
-        *reinterpret_cast<Pack<T, V>*>(p + unit.at0) = x0[i];
-        if (unit.second) *reinterpret_cast<Pack<T, V>*>(p + unit.at1) = x1[i];
+      const int r = r0 + i * slots;
+      if (on && r < rows) {
+        const int t = divided(r, a.head_mul, a.head_shift);
+        T* p = static_cast<T*>(a.out.p) + (first + t) * a.out.token_stride + (r - t * a.n_heads) * a.out.head_stride;
+        if (unit.turns) unit.turn(x0[i], x1[i], s_angle, units, t, a.rope.rot);
+        *reinterpret_cast<P*>(p + unit.at0) = x0[i];
+        if (unit.second) *reinterpret_cast<P*>(p + unit.at1) = x1[i];
       }
     }
+    load(r0 + kAhead * slots);
   }
 }
 
 template <typename T, int V, bool kInter>
 static cudaError_t launch(const RotateArgs& a, cudaStream_t stream) {
   const int units = (a.head_dim + 2 * V - 1) / (2 * V);
-  const int rows = kThreads / units;
-  // Split a token's heads over just enough threads to fill the GPU (148 SMs of
-  // 1024): every slot works the token's angles out again.
-  int slots = 1;
-  while (2 * slots <= rows && slots < a.n_heads && (long long)a.n_tokens * units * slots < 148 * 1024) slots *= 2;
-  const int per_block = rows / slots;
+  const int per_block = rope_tokens_per_block(a.n_tokens, a.n_heads, units, kThreads, kMaxTokens);
   const int blocks = (a.n_tokens + per_block - 1) / per_block;
-  return launch_pdl(rotate_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads), 0, stream, a, units, slots);
+  return launch_pdl(rotate_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads),
+                    (size_t)per_block * units * V * sizeof(float2), stream, a, units, per_block);
 }
 
 // 16-byte packs where the rows and the rotated half allow them, else single

@@ -227,6 +227,7 @@ int kv_rotate(const kv_rope_t* rope, const kv_rows* x, const kv_rows* out, const
     a.n_heads = n_heads;
     a.head_dim = head_dim;
     a.inverse = inverse != 0;
+    pkv::page_divisor(n_heads, &a.head_mul, &a.head_shift);
     const cudaError_t e = pkv::launch_rotate(a, dtype, (cudaStream_t)stream);
     return e == cudaSuccess ? (int)KV_OK : api_cuda_fail(e, "kv_rotate: launch");
   });
@@ -251,6 +252,7 @@ int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int
     a.cu_new = cu_new;
     a.positions = positions;
     a.n_tokens = n_tokens;
+    pkv::page_divisor(c->num_heads, &a.head_mul, &a.head_shift);
     const cudaError_t e = pkv::launch_append_tokens(a, c->dtype, (cudaStream_t)stream);
     return e == cudaSuccess ? (int)KV_OK : api_cuda_fail(e, "kv_append_tokens: launch");
   });

@@ -27,6 +27,8 @@ struct RotateArgs {
   int n_tokens, n_heads, head_dim;
   int inverse;
   int copy_rest;              // out is not x: the values behind rot_dim are copied
+  uint32_t head_mul;          // n_heads as a divisor (page_divisor.h)
+  int head_shift;
   RopeTable rope;
 };
 
@@ -49,6 +51,8 @@ struct AppendTokensArgs {
   const int32_t* cu_new;      // [n_seqs + 1], or NULL: token s is sequence s's
   const int32_t* positions;   // [n_tokens], or NULL: the token's index in its sequence
   int n_tokens;
+  uint32_t head_mul;          // c.H as a divisor
+  int head_shift;
   RopeTable rope;             // rot 0: none
 };
 
