@@ -525,6 +525,14 @@ int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int
  * only. 0 on bad input. */
 size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads);
 
+/* kv_decode_workspace_init -- prepare a workspace (16-byte aligned, of at
+ * least kv_decode_workspace_bytes) for the calls of one batch and number of
+ * query heads; two memsets on `stream`. Calls leave it prepared and keep no
+ * result in it. Calls that may overlap on the GPU, captured ones among them,
+ * need a workspace each.
+ * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY, KV_ERR_CUDA. */
+int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, size_t workspace_bytes, void* stream);
+
 /* kv_decode -- attention of one new token per sequence: for sequence s and
  * query head i, with K/V head i / (q_heads / H),
  *     out[s, i] = sum_j softmax_j(scale q[s, i] . k_j) v_j
@@ -532,9 +540,9 @@ size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads);
  * them). q [n_seqs, q_heads, D], rows on 16-byte boundaries; out
  * [n_seqs, q_heads, D] contiguous, in the pool's dtype. scale 0 is 1/sqrt(D).
  * Rows of length 0 give zeros. fp32 statistics and sums, rounded once; equal
- * inputs give equal bits. workspace (kv_decode_workspace_bytes, 16-byte
- * aligned) needs no initial value and keeps nothing between calls; calls that
- * may overlap on the GPU need one each.
+ * inputs give equal bits. workspace: of kv_decode_workspace_init; one that was
+ * not prepared raises the error word, and sequences split over several CTAs
+ * are then not written. tables and lens must not change while a call runs.
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY (workspace),
  * KV_ERR_CUDA. */
 int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, int window, void* out, void* workspace,

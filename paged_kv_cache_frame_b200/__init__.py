@@ -24,7 +24,7 @@ import ctypes
 from . import capi
 from .capi import KVError, KV_BF16, KV_FP16, KV_FP32, KV_MAX_STREAMS, KV_NOT_CURRENT, KV_STATIC_SCRATCH_BYTES
 from .tokens import (PagedTokens, Rope, kv_append_tokens, kv_decode, kv_decode_append, kv_decode_workspace_bytes,
-                     kv_rope_free, kv_rope_get, kv_rope_init, kv_rope_init_frequencies, kv_rotate, kv_tokens_check)
+                     kv_decode_workspace_init, kv_rope_free, kv_rope_get, kv_rope_init, kv_rope_init_frequencies, kv_rotate, kv_tokens_check)
 
 __all__ = [
     "PagedKVCache", "Plan", "KVError", "workspace_bytes", "KV_BF16", "KV_FP16", "KV_MAX_STREAMS",
@@ -35,7 +35,8 @@ __all__ = [
     "kv_plan_get_stats", "kv_check_device", "kv_testing_fail_launches", "kv_strerror",
     "kv_last_error", "kv_run_static", "kv_set_cross_frame_special", "kv_set_camera_only",
     "Rope", "PagedTokens", "KV_FP32", "kv_rope_init", "kv_rope_init_frequencies", "kv_rope_free", "kv_rope_get",
-    "kv_rotate", "kv_append_tokens", "kv_decode_workspace_bytes", "kv_decode", "kv_decode_append",
+    "kv_rotate", "kv_append_tokens", "kv_decode_workspace_bytes",
+    "kv_decode_workspace_init", "kv_decode", "kv_decode_append",
     "kv_tokens_check",
 ]
 

@@ -132,6 +132,7 @@ SIGNATURES = {
     "kv_rotate": (_I, [_P, _ROWS, _ROWS, _P, _I, _I, _I, _I, _I, _P]),
     "kv_append_tokens": (_I, [_TOKENS, _ROWS, _ROWS, _I, _P, _P, _P, _P]),
     "kv_decode_workspace_bytes": (_SZ, [_TOKENS, _I]),
+    "kv_decode_workspace_init": (_I, [_TOKENS, _I, _P, _SZ, _P]),
     "kv_decode": (_I, [_TOKENS, _ROWS, _I, _F, _I, _P, _P, _SZ, _P]),
     "kv_decode_append": (_I, [_TOKENS, _ROWS, _ROWS, _ROWS, _I, _P, _P, _F, _I, _P, _P, _SZ, _P]),
     "kv_tokens_check": (_I, [_TOKENS, _P]),

@@ -16,7 +16,7 @@ namespace pkv {
 namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 2;         // rows in flight per thread, keys and values
-constexpr int kMaxTokens = 16;    // tokens of a block
+constexpr int kMaxTokens = 8;     // tokens of a block: one per warp for the search
 
 // Sequences s of [0, n) with cu[s + 1] <= t, all before the others: the
 // sequence of token t (n where no sequence holds it). All lanes of a warp.
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid
         back = __ldg(a.cu_new + s + 1) - t;
         if (t < __ldg(a.cu_new + s) || back < 1) {
           s = a.c.n_seqs;
-          if (lane == 0) raise_error(a.c.error);
+          if (lane == 0) raise_error(a.c.error, kErrIndex);
         }
       }
     }
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid
       }
       if (bad) {
         at = -1;
-        if (lane == 0) raise_error(a.c.error);
+        if (lane == 0) raise_error(a.c.error, kErrIndex);
       }
       pos = a.positions ? __ldg(a.positions + t) : j;
     }

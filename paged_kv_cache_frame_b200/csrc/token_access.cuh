@@ -71,14 +71,15 @@ struct Pack<T, 1> {
 };
 
 // Bits of the cache's error word (kv_tokens_check).
-constexpr uint32_t kErrIndex = 2u;
+constexpr uint32_t kErrIndex = 2u;       // a page id, a length or cu_new out of range
+constexpr uint32_t kErrWorkspace = 4u;   // a workspace that was not prepared
 
-__device__ __forceinline__ void raise_error(uint32_t* word) { atomicOr(word, kErrIndex); }
+__device__ __forceinline__ void raise_error(uint32_t* word, uint32_t bit) { atomicOr(word, bit); }
 
 // The length of sequence s, held to what its table can name.
 __device__ __forceinline__ int seq_len(const TokenCache& c, int s) {
   const int n = __ldg(c.lens + s);
-  const int most = c.table_width * c.page_size;   // <= INT32_MAX, checked by the host
+  const int most = c.table_width * c.page_size;   // <= 2^30, checked by the host
   return n < 0 ? 0 : n > most ? most : n;
 }
 __device__ __forceinline__ bool seq_len_bad(const TokenCache& c, int s) {

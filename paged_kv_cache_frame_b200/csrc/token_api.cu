@@ -41,8 +41,10 @@ int view_cache(const kv_tokens* c, const std::string& who, pkv::TokenCache* out)
     return api_fail(KV_ERR_ARG, who + ": max_pages, page_size or num_heads out of range");
   if (c->n_seqs < 0 || c->n_seqs > KV_MAX_TOKEN_SEQS) return api_fail(KV_ERR_ARG, who + ": n_seqs out of range");
   if (c->table_width < 1 || c->table_stride < c->table_width) return api_fail(KV_ERR_ARG, who + ": table_width or table_stride out of range");
-  if ((long long)c->table_width * c->page_size > INT_MAX || (long long)c->max_pages * 2 * c->page_size > INT_MAX)
-    return api_fail(KV_ERR_ARG, who + ": more than 2^31 - 1 tokens a sequence or rows a pool");
+  // The kernels' token indices run up to a tile past a sequence's end, its
+  // rows up to the pool's, both in 31 bits.
+  if ((long long)c->table_width * c->page_size > (1LL << 30) || (long long)c->max_pages * 2 * c->page_size > INT_MAX)
+    return api_fail(KV_ERR_ARG, who + ": more than 2^30 tokens a sequence or 2^31 - 1 rows a pool");
   if (!c->pool || !c->error) return api_fail(KV_ERR_ARG, who + ": NULL pool or error word");
   if (c->n_seqs > 0 && (!c->tables || !c->lens)) return api_fail(KV_ERR_ARG, who + ": NULL tables or lens");
   if (!aligned(c->pool, 16)) return api_fail(KV_ERR_ARG, who + ": pool not 16-byte aligned");
@@ -87,23 +89,25 @@ int view_rope(const kv_rope_t* r, int head_dim, const std::string& who, pkv::Rop
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// [magic | arrival counters | the parts' maxima and sums | their outputs]
 struct DecodeLayout {
   int grid;
-  size_t off_ml, off_meta, total;
+  size_t off_counters, off_ml, off_o, total;
 };
 
 DecodeLayout decode_layout(int D, int group) {
   DecodeLayout l;
-  l.grid = pkv::decode_grid(D, group, pkv::current_device_sms());
+  l.grid = pkv::decode_grid(pkv::current_device_sms());
   const size_t slots = 2 * (size_t)l.grid * pkv::decode_rows(group);
-  l.off_ml = align256(slots * D * 4);
-  l.off_meta = align256(l.off_ml + slots * 8);
-  l.total = align256(l.off_meta + (size_t)l.grid * 16);
+  l.off_counters = 256;
+  l.off_ml = align256(l.off_counters + (size_t)l.grid * 16);
+  l.off_o = align256(l.off_ml + slots * 8);
+  l.total = align256(l.off_o + slots * D * 4);
   return l;
 }
 
 int check_group(const kv_tokens* c, int q_heads, const std::string& who) {
-  // With KV_MAX_TOKEN_SEQS and 2^31 tokens a sequence the bound keeps the
+  // With KV_MAX_TOKEN_SEQS and 2^30 tokens a sequence the bound keeps the
   // kernels' products of tiles and CTAs within 63 bits.
   if (q_heads < 1 || q_heads > KV_MAX_Q_HEADS || q_heads % c->num_heads != 0)
     return api_fail(KV_ERR_ARG, who + ": q_heads must be a multiple of the pool's heads, at most KV_MAX_Q_HEADS");
@@ -135,9 +139,10 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.out = out;
   a.positions = positions;
-  a.part_o = reinterpret_cast<float*>(ws);
+  a.ws_magic = reinterpret_cast<const uint32_t*>(ws);
+  a.counters = reinterpret_cast<uint32_t*>(ws + l.off_counters);
   a.part_ml = reinterpret_cast<float*>(ws + l.off_ml);
-  a.part_meta = reinterpret_cast<int32_t*>(ws + l.off_meta);
+  a.part_o = reinterpret_cast<float*>(ws + l.off_o);
   const int rows = pkv::decode_rows(a.group);
   a.head_groups = (a.group + rows - 1) / rows;
   a.window = window;
@@ -268,6 +273,24 @@ size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads) {
     return 0;
   });
   return n;
+}
+
+int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    const std::string who("kv_decode_workspace_init");
+    pkv::TokenCache view;
+    int rc = view_cache(c, who, &view);
+    if (rc != KV_OK) return rc;
+    if ((rc = check_group(c, q_heads, who)) != KV_OK) return rc;
+    const DecodeLayout l = decode_layout(c->head_dim, q_heads / c->num_heads);
+    if (!workspace || !aligned(workspace, 16)) return api_fail(KV_ERR_ARG, who + ": workspace NULL or not 16-byte aligned");
+    if (workspace_bytes < l.total) return api_fail(KV_ERR_CAPACITY, who + ": workspace smaller than kv_decode_workspace_bytes()");
+    static_assert(pkv::kWorkspaceMagic == 0xa5a5a5a5u, "the magic is one byte over and over");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaError_t e = cudaMemsetAsync(ws + l.off_counters, 0, (size_t)l.grid * 16, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0xa5, 4, (cudaStream_t)stream);
+    return e == cudaSuccess ? (int)KV_OK : api_cuda_fail(e, "kv_decode_workspace_init: memset");
+  });
 }
 
 int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, int window, void* out, void* workspace,

@@ -56,15 +56,18 @@ struct AppendTokensArgs {
   RopeTable rope;             // rot 0: none
 };
 
+constexpr uint32_t kWorkspaceMagic = 0xa5a5a5a5u;
+
 struct DecodeArgs {
   TokenCache c;
   RowsIn q;
   void* out;                  // [n_seqs, q_heads, D] contiguous
   RowsIn k, v;                // the new tokens (fused append), else NULL
   const int32_t* positions;   // [n_seqs], or NULL: len - 1
-  float* part_o;              // [2 * grid][rows][D]
+  const uint32_t* ws_magic;   // kWorkspaceMagic where the workspace was prepared
+  uint32_t* counters;         // [4 * grid] arrivals, zero between launches
   float* part_ml;             // [2 * grid][rows][2]
-  int32_t* part_meta;         // [grid][4]
+  float* part_o;              // [2 * grid][rows][D]
   int group;                  // query heads a K/V head serves
   int head_groups;            // groups of at most `rows` query heads a unit takes
   int window;                 // 0: the whole cache
@@ -77,7 +80,7 @@ cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_append_tokens(const AppendTokensArgs& a, int dtype, cudaStream_t stream);
 // Query heads one unit takes (8 or 16) and CTAs of a launch.
 int decode_rows(int group);
-int decode_grid(int D, int group, int num_sms);
+int decode_grid(int num_sms);
 cudaError_t launch_decode(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
 
 }  // namespace pkv

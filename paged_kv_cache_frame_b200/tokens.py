@@ -75,6 +75,11 @@ def kv_decode_workspace_bytes(tokens, q_heads) -> int:
     return capi.lib().kv_decode_workspace_bytes(tokens, q_heads)
 
 
+def kv_decode_workspace_init(tokens, q_heads, workspace, workspace_bytes, stream=None) -> None:
+    capi.check(capi.lib().kv_decode_workspace_init(tokens, q_heads, workspace, workspace_bytes, stream),
+               "kv_decode_workspace_init")
+
+
 def kv_decode(tokens, q, q_heads, scale, window, out, workspace, workspace_bytes, stream=None) -> None:
     capi.check(capi.lib().kv_decode(tokens, q, q_heads, scale, window, out, workspace, workspace_bytes, stream),
                "kv_decode")
@@ -91,40 +96,49 @@ def kv_tokens_check(tokens, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- tensors
-def _codes():
-    import torch
-    return {torch.bfloat16: KV_BF16, torch.float16: KV_FP16, torch.float32: KV_FP32}
+torch = None    # bound by the first object: importing this package does not import torch
+_codes = {}
+
+
+def _bind_torch():
+    global torch
+    if torch is None:
+        import torch as t
+        _codes.update({t.bfloat16: KV_BF16, t.float16: KV_FP16, t.float32: KV_FP32})
+        torch = t
 
 
 def _check(x, name, shape, dtype, device, contiguous=True):
     """Shape, dtype, layout and device of a tensor, before its address goes to
     the library. Not contiguous: the last dimension only has to be dense."""
+    if (x.shape == shape and x.dtype is dtype and x.device == device
+            and (x.is_contiguous() or (not contiguous and x.stride(-1) == 1))):
+        return
     if tuple(x.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
     if x.dtype != dtype:
         raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
-    if contiguous and not x.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if not contiguous and x.stride(-1) != 1 and x.shape[-1] > 1 and x.numel():
-        raise ValueError(f"{name}: the last dimension must be contiguous")
     if x.device != device:
         raise ValueError(f"{name}: on {x.device}, expected {device}")
+    if contiguous:
+        raise ValueError(f"{name}: must be contiguous")
+    if x.shape[-1] > 1 and x.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
-def _no_grad_inputs(**tensors):
-    import torch
-    if torch.is_grad_enabled():
-        for name, x in tensors.items():
-            if x.requires_grad:
-                raise ValueError(f"{name}: requires a gradient, which this operator does not have "
-                                 "(detach it or call under torch.no_grad)")
+def _no_gradient(*named):
+    for name, x in named:
+        if x.requires_grad:
+            raise ValueError(f"{name}: requires a gradient, which this operator does not have "
+                             "(detach it or call under torch.no_grad)")
 
 
 def _rows(x):
     """kv_rows of a [n, heads, head_dim] tensor; the stride of a dimension of
     one element says nothing and is 0."""
     n, h, _ = x.shape
-    return capi.kv_rows(x.data_ptr(), x.stride(0) if n > 1 else 0, x.stride(1) if h > 1 else 0)
+    t, s, _ = x.stride()
+    return capi.kv_rows(x.data_ptr(), t if n > 1 else 0, s if h > 1 else 0)
 
 
 class _On:
@@ -132,40 +146,41 @@ class _On:
     the call, its outputs and workspace allocated for the stream that uses
     them (torch's current one on that device unless given)."""
 
-    __slots__ = ("stream", "guards")
+    __slots__ = ("stream", "guard")
 
     def __init__(self, device, stream):
-        import torch
-        self.guards = []
         if device.type != "cuda":
             raise ValueError(f"tensors must be on a CUDA device, not on {device}")
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            if stream.device != device:
-                raise ValueError(f"stream on {stream.device}, expected {device}")
-            self.guards.append(torch.cuda.stream(stream))   # makes the device current as well
-            self.stream = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != device.index:
-                self.guards.append(torch.cuda.device(device))
+        if stream is None:
+            self.guard = torch.cuda.device(device)
             self.stream = torch.cuda.current_stream(device).cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, expected {device}")
+        self.guard = torch.cuda.stream(stream)   # makes the device current as well
+        self.stream = stream.cuda_stream
 
     def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
+        self.guard.__enter__()
         return self.stream
 
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+        self.guard.__exit__(*exc)
         return False
+
+
+def _here(device, stream):
+    """The current stream's handle where a call needs no switch of device or
+    stream, else None (_On makes it)."""
+    if stream is None and device.type == "cuda" and torch.cuda.current_device() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
 @functools.lru_cache(maxsize=None)
 def _rotation_with_gradient():
-    import torch
-
     class Rotation(torch.autograd.Function):
         """y = rotation of x; dx = the inverse rotation of dy, itself
         differentiable."""
@@ -174,13 +189,15 @@ def _rotation_with_gradient():
         def forward(ctx, x, positions, rope, inverse):
             ctx.save_for_backward(positions)
             ctx.rope, ctx.inverse = rope, inverse
-            return rope._rotate(x.detach(), positions, None, inverse, None)
+            return rope._rotate(x, positions, None, inverse, None)
 
         @staticmethod
         def backward(ctx, dy):
             positions, = ctx.saved_tensors
             if dy.stride(-1) != 1:
                 dy = dy.contiguous()
+            if not torch.is_grad_enabled():
+                return ctx.rope._rotate(dy, positions, None, not ctx.inverse, None), None, None, None
             return Rotation.apply(dy, positions, ctx.rope, not ctx.inverse), None, None, None
 
     return Rotation
@@ -198,6 +215,7 @@ class Rope:
     def __init__(self, rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_context=0,
                  low_turns=1.0, high_turns=32.0, amplitude=None, inv_freq=None):
         self.handle = None
+        _bind_torch()
         if layout not in LAYOUTS:
             raise ValueError(f"layout: {layout!r}, expected one of {sorted(LAYOUTS)}")
         if scaling not in SCALINGS:
@@ -225,34 +243,41 @@ class Rope:
                 pass
 
     def _rotate(self, x, positions, out, inverse, stream):
-        import torch
-        code = _codes().get(x.dtype)
+        code = _codes.get(x.dtype)
         if code is None:
             raise ValueError(f"x: dtype {x.dtype}, expected bfloat16, float16 or float32")
         if x.dim() != 3:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected [tokens, heads, head_dim]")
-        n, h, d = x.shape
-        _check(x, "x", (n, h, d), x.dtype, x.device, contiguous=False)
-        _check(positions, "positions", (n,), torch.int32, x.device)
+        shape, device = x.shape, x.device
+        _check(x, "x", shape, x.dtype, device, contiguous=False)
+        _check(positions, "positions", shape[:1], torch.int32, device)
         if out is not None:
-            _check(out, "out", (n, h, d), x.dtype, x.device, contiguous=False)
-        with _On(x.device, stream) as s:
-            if out is None:
-                out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
-            kv_rotate(self.handle, _rows(x), _rows(out), positions.data_ptr(), n, h, d, code, inverse, s)
+            _check(out, "out", shape, x.dtype, device, contiguous=False)
+        s = _here(device, stream)
+        if s is not None:
+            return self._launch(x, positions, out, inverse, code, s)
+        with _On(device, stream) as s:
+            return self._launch(x, positions, out, inverse, code, s)
+
+    def _launch(self, x, positions, out, inverse, code, s):
+        n, h, d = x.shape
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        rc = capi.lib().kv_rotate(self.handle, _rows(x), _rows(out), positions.data_ptr(), n, h, d, code, inverse, s)
+        if rc:
+            capi.check(rc, "kv_rotate")
         return out
 
     def rotate(self, x, positions, out=None, inverse=False, stream=None):
         """x [tokens, heads, head_dim] (bfloat16, float16 or float32; the
         last dimension dense) rotated at positions [tokens] (int32), into
         `out` if given (x itself, or apart from it). Differentiable in x."""
-        import torch
-        if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+        if (x.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
             if out is not None or stream is not None:
                 raise ValueError("rotate: out and stream are not for a call that records a gradient "
                                  "(use torch.cuda.stream for the latter)")
             return _rotation_with_gradient().apply(x, positions, self, bool(inverse))
-        return self._rotate(x, positions, out, inverse, stream)
+        return self._rotate(x, positions, out, bool(inverse), stream)
 
 
 class PagedTokens:
@@ -265,7 +290,7 @@ class PagedTokens:
     captures read them anew."""
 
     def __init__(self, pool, tables, lens):
-        import torch
+        _bind_torch()
         if pool.dim() != 5 or pool.shape[1] != 2:
             raise ValueError(f"pool: shape {tuple(pool.shape)}, expected [max_pages, 2, page_size, heads, head_dim]")
         if pool.dtype not in (torch.bfloat16, torch.float16):
@@ -280,12 +305,14 @@ class PagedTokens:
         _check(lens, "lens", (self.n_seqs,), torch.int32, pool.device)
         self.pool, self.tables, self.lens = pool, tables, lens
         self.max_pages, _, self.page_size, self.H, self.D = pool.shape
+        self._dtype, self._device = pool.dtype, pool.device
         self.error = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._c = capi.kv_tokens(
             pool.data_ptr(), tables.data_ptr(), lens.data_ptr(), self.error.data_ptr(),
             tables.stride(0) if self.n_seqs > 1 else width, self.max_pages, self.page_size, self.H, self.D,
-            _codes()[pool.dtype], width, self.n_seqs)
-        self._ws = {}   # query heads -> workspace bytes
+            _codes[pool.dtype], width, self.n_seqs)
+        self._bytes = {}        # query heads -> workspace bytes
+        self._workspaces = {}   # (stream, query heads) -> the workspace of eager calls there
 
     @classmethod
     def of_plan(cls, plan, block, streams=None):
@@ -294,7 +321,7 @@ class PagedTokens:
         (default all), whose pools must be one (a group's, or one cache's).
         Tables and lengths are copies: they hold until a cache's page state
         changes. Refused where pages hold tokens that the plan hides."""
-        import torch
+        _bind_torch()
         streams = list(range(len(plan.caches))) if streams is None else list(streams)
         if not streams:
             raise ValueError("streams: none given")
@@ -320,15 +347,10 @@ class PagedTokens:
                    torch.tensor([t + [0] * (width - len(t)) for t in tables], dtype=torch.int32, device=pool.device),
                    torch.tensor(lens, dtype=torch.int32, device=pool.device))
 
-    def _new(self, k, v, n):
-        for x, name in ((k, "k"), (v, "v")):
-            _check(x, name, (n, self.H, self.D), self.pool.dtype, self.pool.device, contiguous=False)
-
     def _index(self, x, name, n):
-        import torch
         if x is None:
             return None
-        _check(x, name, (n,), torch.int32, self.pool.device)
+        _check(x, name, (n,), torch.int32, self._device)
         return x.data_ptr()
 
     def append(self, k, v, cu_new=None, rope=None, positions=None, stream=None):
@@ -336,75 +358,123 @@ class PagedTokens:
         rotated by `rope` at `positions` [tokens] (default: their index in the
         sequence). cu_new [n_seqs + 1]: tokens cu_new[s] .. cu_new[s + 1] - 1
         are the last of sequence s (None: one each)."""
-        _no_grad_inputs(k=k, v=v)
-        n = k.shape[0] if k.dim() == 3 and cu_new is not None else self.n_seqs
-        self._new(k, v, n)
+        n = self.n_seqs if cu_new is None or k.dim() != 3 else k.shape[0]
+        shape = (n, self.H, self.D)
+        _check(k, "k", shape, self._dtype, self._device, contiguous=False)
+        _check(v, "v", shape, self._dtype, self._device, contiguous=False)
+        if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+            _no_gradient(("k", k), ("v", v))
         cu = self._index(cu_new, "cu_new", self.n_seqs + 1)
         pos = self._index(positions, "positions", n)
-        with _On(self.pool.device, stream) as s:
-            kv_append_tokens(self._c, _rows(k), _rows(v), n, cu, rope.handle if rope is not None else None, pos, s)
+        s = _here(self._device, stream)
+        if s is not None:
+            return self._append(k, v, n, cu, rope, pos, s)
+        with _On(self._device, stream) as s:
+            return self._append(k, v, n, cu, rope, pos, s)
+
+    def _append(self, k, v, n, cu, rope, pos, s):
+        rc = capi.lib().kv_append_tokens(self._c, _rows(k), _rows(v), n, cu, rope.handle if rope is not None else None,
+                                         pos, s)
+        if rc:
+            capi.check(rc, "kv_append_tokens")
 
     def workspace_bytes(self, q_heads) -> int:
         """Bytes of a workspace for decode and decode_append."""
-        if q_heads not in self._ws:
-            with _On(self.pool.device, None):
-                self._ws[q_heads] = kv_decode_workspace_bytes(self._c, q_heads)
-        return self._ws[q_heads]
+        if q_heads not in self._bytes:
+            with torch.cuda.device(self._device):
+                self._bytes[q_heads] = kv_decode_workspace_bytes(self._c, q_heads)
+        return self._bytes[q_heads]
 
-    def _queries(self, q, out, workspace, scale):
-        import torch
+    def workspace(self, q_heads, stream=None):
+        """A prepared workspace for decode and decode_append with that many
+        query heads. Calls that may overlap on the GPU need one each; those
+        without a given one share one per stream."""
+        with _On(self._device, stream) as s:
+            return self._new_workspace(q_heads, s)
+
+    def _new_workspace(self, q_heads, s):
+        ws = torch.empty(self.workspace_bytes(q_heads), dtype=torch.uint8, device=self._device)
+        kv_decode_workspace_init(self._c, q_heads, ws.data_ptr(), ws.numel(), s)
+        return ws
+
+    def _check_call(self, q, out, scale, workspace):
         if q.dim() != 3:
             raise ValueError(f"q: shape {tuple(q.shape)}, expected [n_seqs, q heads, head_dim]")
         heads = q.shape[1]
-        _check(q, "q", (self.n_seqs, heads, self.D), self.pool.dtype, self.pool.device, contiguous=False)
+        shape = (self.n_seqs, heads, self.D)
+        _check(q, "q", shape, self._dtype, self._device, contiguous=False)
         if heads < 1 or heads % self.H:
             raise ValueError(f"q: {heads} heads, expected a multiple of the pool's {self.H}")
         if out is not None:
-            _check(out, "out", (self.n_seqs, heads, self.D), self.pool.dtype, self.pool.device)
+            _check(out, "out", shape, self._dtype, self._device)
         if scale is not None and not scale:
             raise ValueError("scale: 0 would weigh all tokens alike")
-        if workspace is not None and (workspace.device != self.pool.device or not workspace.is_contiguous()):
+        if workspace is not None and (workspace.device != self._device or not workspace.is_contiguous()):
             raise ValueError("workspace: must be contiguous, on the pool's device")
-        return heads
 
-    def _buffers(self, q, heads, out, workspace):
-        import torch
+    def _buffers(self, q, out, workspace, s):
         if out is None:
-            out = torch.empty((self.n_seqs, heads, self.D), dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if workspace is None:
-            workspace = torch.empty(self.workspace_bytes(heads), dtype=torch.uint8, device=q.device)
+            heads = q.shape[1]
+            if torch.cuda.is_current_stream_capturing():
+                workspace = self._new_workspace(heads, s)   # the graph's own, prepared by each replay
+            else:
+                workspace = self._workspaces.get((s, heads))
+                if workspace is None:
+                    workspace = self._workspaces[s, heads] = self._new_workspace(heads, s)
         return out, workspace
 
     def decode(self, q, out=None, scale=None, window=0, workspace=None, stream=None):
         """Attention of one new token per sequence: q [n_seqs, q heads,
         head_dim] against the sequence's last `window` tokens (0: all). scale:
-        default 1/sqrt(head_dim). workspace (workspace_bytes(q heads)): one
-        per call unless given."""
-        _no_grad_inputs(q=q)
-        heads = self._queries(q, out, workspace, scale)
-        with _On(self.pool.device, stream) as s:
-            out, ws = self._buffers(q, heads, out, workspace)
-            kv_decode(self._c, _rows(q), heads, 0.0 if scale is None else scale, window, out.data_ptr(),
-                      ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        default 1/sqrt(head_dim). workspace: of workspace() (default: one per
+        stream, in a capture one per call, prepared by the graph)."""
+        self._check_call(q, out, scale, workspace)
+        if q.requires_grad and torch.is_grad_enabled():
+            _no_gradient(("q", q))
+        s = _here(self._device, stream)
+        if s is not None:
+            return self._decode(q, out, scale, window, workspace, s)
+        with _On(self._device, stream) as s:
+            return self._decode(q, out, scale, window, workspace, s)
+
+    def _decode(self, q, out, scale, window, workspace, s):
+        out, ws = self._buffers(q, out, workspace, s)
+        rc = capi.lib().kv_decode(self._c, _rows(q), q.shape[1], scale or 0.0, window, out.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), s)
+        if rc:
+            capi.check(rc, "kv_decode")
         return out
 
     def decode_append(self, k, v, q, rope=None, positions=None, out=None, scale=None, window=0, workspace=None,
                       stream=None):
         """A decode step: append(k, v, rope=rope), rotate q at the same
-        positions [n_seqs] (default lens - 1) and decode(q), in one go."""
-        _no_grad_inputs(k=k, v=v, q=q)
-        self._new(k, v, self.n_seqs)
-        heads = self._queries(q, out, workspace, scale)
+        positions [n_seqs] (default lens - 1) and decode(q), in one launch."""
+        shape = (self.n_seqs, self.H, self.D)
+        _check(k, "k", shape, self._dtype, self._device, contiguous=False)
+        _check(v, "v", shape, self._dtype, self._device, contiguous=False)
+        self._check_call(q, out, scale, workspace)
+        if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+            _no_gradient(("k", k), ("v", v), ("q", q))
         pos = self._index(positions, "positions", self.n_seqs)
-        with _On(self.pool.device, stream) as s:
-            out, ws = self._buffers(q, heads, out, workspace)
-            kv_decode_append(self._c, _rows(k), _rows(v), _rows(q), heads,
-                             rope.handle if rope is not None else None, pos, 0.0 if scale is None else scale,
-                             window, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        s = _here(self._device, stream)
+        if s is not None:
+            return self._decode_append(k, v, q, rope, pos, out, scale, window, workspace, s)
+        with _On(self._device, stream) as s:
+            return self._decode_append(k, v, q, rope, pos, out, scale, window, workspace, s)
+
+    def _decode_append(self, k, v, q, rope, pos, out, scale, window, workspace, s):
+        out, ws = self._buffers(q, out, workspace, s)
+        rc = capi.lib().kv_decode_append(self._c, _rows(k), _rows(v), _rows(q), q.shape[1],
+                                         rope.handle if rope is not None else None, pos, scale or 0.0, window,
+                                         out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        if rc:
+            capi.check(rc, "kv_decode_append")
         return out
 
     def check_device(self, stream=None):
         """Synchronise and raise KVError if a kernel met a page id or length
         out of range since the last check."""
-        with _On(self.pool.device, stream) as s:
+        with _On(self._device, stream) as s:
             kv_tokens_check(self._c, s)

@@ -555,7 +555,7 @@ def test_captured_steps_follow_the_lengths(pkv):
     for x in (b, eager):
         x.len_t.copy_(torch.tensor(lens, dtype=torch.int32))
     q, k, v = randn((4, 8, 128), b.dtype, b.g), randn((4, 2, 128), b.dtype, b.g), randn((4, 2, 128), b.dtype, b.g)
-    ws = torch.empty(b.cache.workspace_bytes(8), dtype=torch.uint8, device="cuda").fill_(255)
+    ws = b.cache.workspace(8)
     side = torch.cuda.Stream()
     outs, graphs = [torch.zeros_like(q) for _ in range(2)], []
     side.wait_stream(torch.cuda.current_stream())
@@ -572,6 +572,10 @@ def test_captured_steps_follow_the_lengths(pkv):
             else:
                 b.cache.decode_append(k, v, q, rope=rope, out=outs[i], workspace=ws)
         graphs.append(graph)
+    own = torch.zeros_like(q)                       # and one with a workspace of the graph's
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        own.copy_(b.cache.decode(q))
     for step in range(30):
         live = (b.len_t > 0).int()
         b.len_t += live
@@ -585,6 +589,34 @@ def test_captured_steps_follow_the_lengths(pkv):
         else:
             want = eager.cache.decode_append(k, v, q, rope=rope)
         assert torch.equal(outs[step % 2], want), step
+        graph.replay()
+        assert torch.equal(own, eager.cache.decode(q)), step
+    b.cache.check_device()
+
+
+def test_unprepared_workspace_is_reported(pkv):
+    b = Batch(pkv, [9000], 1, 64, 64, seed=23)
+    q = randn((1, 2, 64), b.dtype, b.g)
+    ws = torch.zeros(b.cache.workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    b.cache.decode(q, workspace=ws)
+    with pytest.raises(pkv.KVError) as e:
+        b.cache.check_device()
+    assert e.value.name == "DEVICE_CHECK"
+    pkv.kv_decode_workspace_init(b.cache._c, 2, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert_attended(b.cache.decode(q, workspace=ws), b, q)
+    b.cache.check_device()
+
+
+@pytest.mark.parametrize("seqs,hkv,g,n", [(1, 1, 1, 70000), (1, 1, 16, 40000), (2, 1, 5, 30000), (5, 1, 3, 9000), (1, 3, 2, 20011)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_parts(pkv, seqs, hkv, g, n, d):
+    """Units of up to 296 parts: joined in one round and in two, full groups and ragged ones."""
+    b = Batch(pkv, [n - 1000 * i for i in range(seqs)], hkv, d, 128, seed=24)
+    q = randn((seqs, hkv * g, d), b.dtype, b.g)
+    out = b.cache.decode(q, scale=0.3)              # weights peaked enough for every part's to matter
+    assert_attended(out, b, q, scale=0.3)
+    for _ in range(5):
+        assert torch.equal(out, b.cache.decode(q, scale=0.3))
     b.cache.check_device()
 
 
@@ -651,10 +683,10 @@ def test_refused_calls(pkv):
     with pytest.raises(pkv.KVError) as e:
         b.cache.decode(q, window=-1)
     assert e.value.name == "ARG"
-    for fails in (1, 2):                            # the second launch of a call
+    for call in (lambda: b.cache.decode(q), lambda: b.cache.decode_append(k, k, q), lambda: b.cache.append(k, k)):
         pkv.kv_testing_fail_launches(1)
         with pytest.raises(pkv.KVError) as e:
-            b.cache.decode(q)
+            call()
         assert e.value.name == "CUDA"
     assert_attended(b.cache.decode(q), b, q)
 

@@ -113,7 +113,7 @@ BAD_TOKENS = [
     ({"n_seqs": -1}, "ARG"), ({"n_seqs": 16385}, "ARG"), ({"table_width": 0}, "ARG"), ({"table_stride": 3}, "ARG"),
     ({"pool": None}, "ARG"), ({"pool": 4104}, "ARG"), ({"tables": None}, "ARG"), ({"lens": None}, "ARG"),
     ({"error": None}, "ARG"), ({"error": 4098}, "ARG"), ({"tables": 4097}, "ARG"),
-    ({"table_width": 1 << 20, "table_stride": 1 << 20, "page_size": 4096}, "ARG"),
+    ({"table_width": 1 << 20, "table_stride": 1 << 20, "page_size": 1025}, "ARG"),
     ({"max_pages": 1 << 20, "page_size": 1024}, "ARG")]
 
 
@@ -155,6 +155,9 @@ def test_decode_refusals(pkv):
         assert code(pkv, pkv.kv_decode_append, c, k, v, r, 2, rope, pos, 0.0, 0, 4096, 4096, big) == "ARG"
     assert code(pkv, pkv.kv_tokens_check, None) == "ARG"
     assert pkv.kv_decode_workspace_bytes(c, 3) == 0
+    for args, want in [((None, 2, 4096, big), "ARG"), ((c, 3, 4096, big), "ARG"), ((c, 2, None, big), "ARG"),
+                       ((c, 2, 4104, big), "ARG"), ((c, 2, 4096, need - 1), "CAPACITY")]:
+        assert code(pkv, pkv.kv_decode_workspace_init, *args) == want
 
 
 def test_rotate_refusals(pkv):
@@ -263,62 +266,68 @@ def test_sequence_search():
         assert 0 <= find_seq(cu, n, rng.randint(0, 50)) <= n
 
 
-def line_parts(tiles, units, grid):
-    """(unit key, CTA, slot, first tile, last tile) of every piece, as the
-    attention kernel cuts the line, and the parts its last pieces announce."""
+JOIN, GROUP = 32, 16   # parts joined in one round, and neighbours joined first where there are more
+
+
+def line_pieces(tiles, units, grid):
+    """The pieces of every CTA as the attention kernel cuts the line: unit
+    key, CTA, tiles, and of a split unit its slot, first CTA and parts."""
     total = sum(t * units for t in tiles)
     parts = min(grid, total)
-    pieces, meta = [], {}
+    pieces = []
     for c in range(parts):
-        t, end = c * total // parts, (c + 1) * total // parts
-        base, seq = 0, 0
-        while not (tiles[seq] * units and base <= t < base + tiles[seq] * units):
-            base += tiles[seq] * units
-            seq += 1
-        meta[c] = 0
+        t, end, base, seq = c * total // parts, (c + 1) * total // parts, 0, 0
         while t < end:
-            n = tiles[seq]
-            unit, t0 = divmod(t - base, n)
-            t1 = n if n - t0 < end - t else t0 + end - t
-            whole = t0 == 0 and t1 == n
-            opens = t0 == 0 and not whole
-            pieces.append(((seq, unit), c, None if whole else 2 * c + (1 if opens else 0), t0, t1))
-            if opens:
-                last = base + (unit + 1) * n - 1
-                meta[c] = ((last + 1) * parts - 1) // total - c + 1
-            t += t1 - t0
-            if t >= base + n * units and t < end:
-                base += n * units
+            while t >= base + tiles[seq] * units:
+                base += tiles[seq] * units
                 seq += 1
-                while tiles[seq] == 0:
-                    seq += 1
-    return pieces, meta
+            n = tiles[seq]
+            unit = (t - base) // n
+            unit_base = base + unit * n
+            t0 = t - unit_base
+            t1 = n if n - t0 < end - t else t0 + end - t
+            split = None
+            if t0 > 0 or t1 < n:
+                c0 = ((unit_base + 1) * parts - 1) // total
+                split = (2 * c + (1 if c == c0 else 0), c0, ((unit_base + n) * parts - 1) // total - c0 + 1)
+            pieces.append(((seq, unit), c, t0, t1, split))
+            t += t1 - t0
+    return pieces
 
 
 @pytest.mark.parametrize("seed", range(60))
 def test_split_covers_every_tile_and_the_join_finds_the_parts(seed):
+    """Every tile once; a unit's parts in the slots the join reads; arrivals
+    counted to the number that comes, on counters no two units share."""
     rng = random.Random(seed)
     seqs, units, grid = rng.choice([1, 2, 7, 64, 300]), rng.choice([1, 2, 8, 24]), rng.choice([1, 4, 296])
     tiles = [rng.choice([0, 1, 2, 5, rng.randint(0, 400)]) for _ in range(seqs)]
     if not sum(tiles):
         tiles[-1] = 1
-    pieces, meta = line_parts(tiles, units, grid)
-    by_unit, used = {}, set()
-    for key, c, slot, t0, t1 in pieces:
-        by_unit.setdefault(key, []).append((t0, t1, c, slot))
-        if slot is not None:
-            assert slot < 2 * grid and slot not in used
-            used.add(slot)
-    assert set(by_unit) == {(s, u) for s in range(seqs) if tiles[s] for u in range(units)}
-    joined = set()
+    pieces = line_pieces(tiles, units, grid)
+    assert set(k for k, *_ in pieces) == {(s, u) for s in range(seqs) if tiles[s] for u in range(units)}
+    by_unit, slots, first, second = {}, set(), {}, {}
+    for key, c, t0, t1, split in pieces:
+        by_unit.setdefault(key, []).append((t0, t1, c, split))
+        if split:
+            slot, c0, n = split
+            assert slot < 2 * grid and slot not in slots
+            slots.add(slot)
+            two, me = n > JOIN, c - c0
+            g0 = me // GROUP * GROUP if two else 0
+            counter = 2 * (c0 + g0) + (1 if g0 == 0 else 0)
+            of = min(GROUP, n - g0) if two else n
+            first.setdefault(counter, []).append((key, of))
+            if two and me == g0:
+                second.setdefault(2 * c0 + 1, []).append((key, (n + GROUP - 1) // GROUP))
+    for counters in (first, second):
+        for arrivals in counters.values():
+            assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][1] <= JOIN
     for (seq, _), p in by_unit.items():
-        p.sort()
+        p.sort(key=lambda x: x[:3])
         assert p[0][0] == 0 and p[-1][1] == tiles[seq] and all(a[1] == b[0] for a, b in zip(p, p[1:]))
         if len(p) > 1:
-            c = p[0][2]
-            assert meta[c] == len(p)
-            assert [x[3] for x in p] == [2 * (c + i) + (1 if i == 0 else 0) for i in range(len(p))]
-            joined.add(c)
+            c0 = p[0][2]
+            assert [x[3] for x in p] == [(2 * (c0 + i) + (1 if i == 0 else 0), c0, len(p)) for i in range(len(p))]
         else:
             assert p[0][3] is None
-    assert joined == {c for c, n in meta.items() if n}
