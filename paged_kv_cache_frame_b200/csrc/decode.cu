@@ -8,22 +8,28 @@
 // query heads that shares it.
 //
 // Split. A unit is one (sequence, K/V head, group of at most `rows` query
-// heads); its tokens are cut into tiles, all units' tiles stand in one line,
-// and CTA c of G takes the c-th G-th of the line, whatever the sequences'
-// lengths: no CTA waits for a long sequence. The lengths are read on the
-// device, so a captured launch serves growing sequences. A unit that lies in
-// one CTA is written to `out` by it; of the others every CTA leaves (max,
-// sum, unnormalised O) in the workspace, and the CTA that arrives last joins
-// them, in their order along the sequence whichever CTA that is: results do
-// not depend on timing, and no CTA waits for another. More than kJoin parts
-// are joined in two rounds, kGroup neighbours first.
+// heads); its tokens are cut into tiles. Every CTA works its own part of the
+// split out from the lengths, which are read on the device, so a captured
+// launch serves growing sequences:
+//   - while cutting every unit into parts of at most kPartTiles tiles gives no
+//     more parts than CTAs, each part is a CTA's: short units stay whole, and
+//     nothing is joined that would not pay for it;
+//   - else all units' tiles (and kUnitCost more each, for what a unit costs by
+//     itself) stand in one line, and CTA c of G takes the c-th G-th of it,
+//     whatever the sequences' lengths: no CTA waits for a long sequence.
+// A unit that lies in one CTA is written to `out` by it; of the others every
+// CTA leaves (max, sum, unnormalised O) in the workspace, and the CTA that
+// arrives last joins them, in their order along the sequence whichever CTA
+// that is: results do not depend on timing, and no CTA waits for another.
+// More than kJoin parts are joined in two rounds, kGroup neighbours first.
 //
 // In a CTA each warp takes every kWarps-th step of kStep tokens and keeps a
 // running max, sum and O of its own; no warp waits for another until the end
 // of the unit. Token rows are gathered by 16-byte asynchronous copies into a
 // ring per warp (rows past the end are zero-filled and masked, so what the
 // pool holds there is never read). The ring runs on into the CTA's next unit
-// while the warps of this one are joined.
+// while the warps of this one are joined, and the next unit's queries (and
+// new key and value) are in registers by then.
 //
 // The products run transposed on mma.sync m16n8k16, the query heads on the
 // N = 8 side: S^T = K Q^T (tokens x heads) and O^T += V^T P^T. K and V then
@@ -46,6 +52,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
+constexpr float kSlack = 8.f;   // growth of a score, in powers of two, that the running max lets pass
+constexpr int kPartTiles = 3;   // tiles (32 KB of K and V each) that are not worth a join
+constexpr int kUnitCost = 3;    // a unit's own cost in tiles
 constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
 constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
@@ -53,7 +62,7 @@ template <int D>
 struct Shape {
   static constexpr int kM = D == 64 ? 2 : 1;            // 16-token blocks of a step
   static constexpr int kStep = 16 * kM;                 // tokens a warp takes at a time (8 KB of K and V)
-  static constexpr int kTileTokens = kStep * kWarps;    // tokens of a tile of the split
+  static constexpr int kStride = kStep * kWarps;        // tokens of a step of all warps, and of the finest tile
   static constexpr int kStages = 3;
   static constexpr int kHalf = kStep * D * 2;           // K (or V) bytes of a stage
   static constexpr int kRing = kWarps * kStages * 2 * kHalf;
@@ -76,41 +85,17 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// First token and number of tokens that sequence s's query sees.
-__device__ __forceinline__ void span(const DecodeArgs& a, int s, int& first, int& len) {
-  len = seq_len(a.c, s);
-  first = a.window > 0 && len > a.window ? len - a.window : 0;
+// The first token that the query of a sequence of `len` sees, and the tiles
+// of each of its units.
+__device__ __forceinline__ int first_seen(const DecodeArgs& a, int len) {
+  return a.window > 0 && len > a.window ? len - a.window : 0;
 }
-template <int kTileTokens>
-__device__ __forceinline__ int seq_tiles(const DecodeArgs& a, int s) {
-  int first, len;
-  span(a, s, first, len);
-  return (int)(((long long)(len - first) + kTileTokens - 1) / kTileTokens);
+__device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, int len) {
+  return ((uint32_t)(len - first_seen(a, len)) + (1u << a.tile_shift) - 1) >> a.tile_shift;
 }
 
-// Sum of v over the block (kThreads threads), and the inclusive sum up to the
-// calling thread.
-__device__ __forceinline__ long long block_scan(long long v, long long* scratch, long long& total) {
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  if (lane == 31) scratch[w] = v;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) v += scratch[i];
-    total += scratch[i];
-  }
-  __syncthreads();
-  return v;
-}
-
-// Shared memory behind the rings. The rotated queries of a unit and the
-// join's weights and sums take the place of the warps' O: never at once.
+// Shared memory behind the rings. A unit's queries (as they come, and
+// rotated) take the place of the warps' O: never at once.
 template <int D, int NT>
 struct Smem {
   static constexpr int kRows = 8 * NT;
@@ -118,7 +103,8 @@ struct Smem {
   static constexpr int kOffMl = kOffO + kWarps * 8 * D * 4;            // [warp][8 heads] (max, sum)
   static constexpr int kOffNew = kOffMl + kWarps * 8 * 8;              // fused: new key and value [2][D]
   static constexpr int kBytes = kOffNew + 2 * D * 2;
-  static_assert(kRows * D * 4 <= kWarps * 8 * D * 4, "the queries fit the warps' O");
+  static constexpr int kOffTurned = kOffO + kRows * D * 2;             // queries [row][D] fp32, behind them as they came
+  static_assert(kRows * D * 6 <= kWarps * 8 * D * 4, "the queries fit the warps' O");
 };
 
 // Element d of row i of a warp's O block: row i shifted by 4 i floats, so
@@ -142,148 +128,196 @@ __device__ __forceinline__ bool rope_pair(const RopeTable& t, int p, int& e0, in
   return on;
 }
 
-// A CTA's part of the line.
-struct Line {
-  long long t, end;   // tiles [t, end) of the line are left
-  long long base;     // the line's index of sequence seq's first tile
+// How the tiles are split over the CTAs (above), and what is left of this
+// CTA's part. The host chooses tiles coarse enough for 31 bits.
+struct Split {
+  bool by_parts;      // a part a CTA; else the line
+  uint32_t each, more;   // the line: CTAs below `more` take each + 1 places, the others `each`
+  uint32_t t, end;    // places [t, end) of the line (or parts of all units) are left
+  uint32_t base;      // the first place of sequence seq
   int seq;
-};
+  int len, later;     // the lengths of seq and seq + 1: read a sequence ahead, as a load takes
+                      // about a microsecond while the memory is busy
 
-// The tiles of one unit that the CTA takes.
-struct Piece {
-  int seq, first, len;      // tokens [first, len) are seen
-  int unit, tiles;          // the unit in its sequence, and its tiles
-  int tile0, tile1;
-  long long unit_base;      // the line's index of its first tile
-};
-
-template <int kTileTokens>
-__device__ __forceinline__ bool next_piece(const DecodeArgs& a, int units, Line& l, Piece& p) {
-  if (l.t >= l.end) return false;
-  for (; l.seq < a.c.n_seqs; ++l.seq) {
-    p.tiles = seq_tiles<kTileTokens>(a, l.seq);
-    const long long n = (long long)p.tiles * units;
-    if (l.t < l.base + n) break;
-    l.base += n;
+  __device__ __forceinline__ uint32_t cta_of(uint32_t place) const {
+    const uint32_t lower = more * (each + 1);
+    return place < lower ? place / (each + 1) : more + (place - lower) / each;
   }
-  if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
-  p.seq = l.seq;
-  span(a, l.seq, p.first, p.len);
-  p.unit = (int)((l.t - l.base) / p.tiles);
-  p.unit_base = l.base + (long long)p.unit * p.tiles;
-  p.tile0 = (int)(l.t - p.unit_base);
-  p.tile1 = (int)(p.tiles - p.tile0 < l.end - l.t ? p.tiles : p.tile0 + (l.end - l.t));
-  l.t += p.tile1 - p.tile0;
-  return true;
+};
+
+// The tokens of one unit that the CTA takes.
+struct Piece {
+  int seq, len;       // and the sequence's length
+  int unit;           // the unit in its sequence
+  int tok0, tok1;     // tokens [tok0, tok1)
+  int c0, parts;      // the unit's first CTA, and in how many it lies
+};
+
+__device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
+  return s < a.c.n_seqs ? __ldg(a.c.lens + s) : 0;
 }
+__device__ __forceinline__ uint32_t parts_of(uint32_t tiles) { return (tiles + kPartTiles - 1) / kPartTiles; }
+
+__device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t units, Split& l, Piece& p) {
+  while (l.t < l.end) {
+    uint32_t tiles = 0, size = 0;   // places of a unit
+    for (; l.seq < a.c.n_seqs; ++l.seq) {
+      tiles = tiles_of(a, l.len);
+      size = l.by_parts ? parts_of(tiles) : tiles ? tiles + kUnitCost : 0;
+      if (l.t - l.base < size * units) break;
+      l.base += size * units;
+      l.len = held(a.c, l.later);
+      l.later = raw_len(a, l.seq + 2);
+    }
+    if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
+    const uint32_t off = l.t - l.base, unit = off / size, at = off - unit * size;
+    uint32_t tile0, tile1;
+    if (l.by_parts) {
+      tile0 = (uint32_t)((unsigned long long)tiles * at / size);
+      tile1 = (uint32_t)((unsigned long long)tiles * (at + 1) / size);
+      p.c0 = l.t - at;
+      p.parts = size;
+      ++l.t;
+    } else {
+      const uint32_t n = min(l.end - l.t, size - at);
+      tile0 = at > kUnitCost ? at - kUnitCost : 0;
+      tile1 = at + n > kUnitCost ? at + n - kUnitCost : 0;
+      const uint32_t first = l.t - at;
+      p.c0 = l.cta_of(first + kUnitCost);
+      p.parts = l.cta_of(first + size - 1) - p.c0 + 1;
+      l.t += n;
+    }
+    if (tile0 == tile1) continue;
+    p.seq = l.seq;
+    p.unit = unit;
+    p.len = l.len;
+    const int first = first_seen(a, l.len);
+    p.tok0 = first + (int)(tile0 << a.tile_shift);
+    p.tok1 = tile1 == tiles ? p.len : first + (int)(tile1 << a.tile_shift);
+    return true;
+  }
+  return false;
+}
+
+// This CTA's part of the split. Each warp works it out by itself, a lane for
+// a stretch of the sequences.
+__device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t units) {
+  const int lane = threadIdx.x % 32;
+  const int stretch = (a.c.n_seqs + 31) / 32;
+  const int s0 = min(lane * stretch, a.c.n_seqs), s1 = min(s0 + stretch, a.c.n_seqs);
+  unsigned long long mine = 0;   // places of the line below, parts above
+  for (int s = s0; s < s1; ++s) {
+    const uint32_t tiles = tiles_of(a, seq_len(a.c, s));
+    mine += (unsigned long long)parts_of(tiles) << 32 | (tiles ? tiles + kUnitCost : 0);
+  }
+  mine *= units;                 // both stay below 2^31
+  unsigned long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const unsigned long long total = __shfl_sync(0xffffffffu, upto, 31);
+  Split l;
+  l.by_parts = (total >> 32) <= (uint32_t)a.grid;
+  const uint32_t c = blockIdx.x;
+  if (l.by_parts) {
+    l.t = min(c, (uint32_t)(total >> 32));
+    l.end = min(c + 1, (uint32_t)(total >> 32));
+    l.each = l.more = 0;
+  } else {
+    const uint32_t n = (uint32_t)total, g = a.grid;   // more places than CTAs
+    l.each = n / g;
+    l.more = n - l.each * g;
+    l.t = c * l.each + min(c, l.more);
+    l.end = l.t + l.each + (c < l.more ? 1 : 0);
+  }
+  const uint32_t last = l.by_parts ? (uint32_t)(upto >> 32) : (uint32_t)upto;
+  const uint32_t size = l.by_parts ? (uint32_t)(mine >> 32) : (uint32_t)mine;
+  const uint32_t here = __ballot_sync(0xffffffffu, l.t < last && l.t >= last - size);
+  const int owner = here ? __ffs(here) - 1 : 31;
+  l.seq = __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner);
+  l.base = __shfl_sync(0xffffffffu, last - size, owner);
+  l.len = held(a.c, raw_len(a, l.seq));
+  l.later = raw_len(a, l.seq + 1);
+  return l;   // next_piece goes on from the stretch's first sequence
+}
+
+// A split unit's part that this CTA holds: the unit's first CTA, its parts,
+// its query heads and the first one's row of `out`.
+struct Part {
+  int c0, parts, heads, row;
+};
 
 // A part of a unit: CTA c0 + p's, in that CTA's second slot if it opened the
 // unit, else in its first.
 __device__ __forceinline__ long long part_slot(int c0, int p) { return 2LL * (c0 + p) + (p == 0 ? 1 : 0); }
 
-// Adds one to a counter; the arrival that completes `of` sets it back to zero
-// and returns true, with the others' writes visible. Called by one thread
-// after a barrier behind the CTA's writes.
+// Adds one to a counter; true for the arrival that completes `of`, with the
+// others' writes visible to it. Called by one thread, after a barrier behind
+// the CTA's writes.
 __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
-  fence_acq_rel_gpu();
-  const bool last = atomicAdd(counter, 1u) == (uint32_t)(of - 1);
-  if (last) {
-    atomicExch(counter, 0u);
-    fence_acq_rel_gpu();
-  }
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  const bool last = old == (uint32_t)(of - 1);
+  if (last) *counter = 0;   // for the next launch
   return last;
 }
 
 // Joins parts p0, p0 + step, ... (n of at most 32) of the unit begun by CTA
 // c0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
 // writes O / l to `out` (the unit's first query row), others the part in the
-// first one's place. A lane per part works the weights out; the rows' 16-byte
-// pieces are spread over the threads, several lanes of parts to a piece where
-// there are threads to spare.
+// first one's place. A warp takes a query head at a time, a lane a part's
+// weight, then all lanes the parts' rows with kPre of them in flight, the
+// first before the weights are known.
 template <int D, typename T, int kRows>
-__device__ __forceinline__ void join_parts(const DecodeArgs& a, float* smem, int c0, int p0, int step, int n, int heads,
-                                           T* out) {
-  constexpr int kPieces = D / 4;   // of a row
-  constexpr int kPre = 8;          // parts requested before the weights are known
-  float* s_f = smem;                                        // [part][row]
-  float* s_l = s_f + 32 * kRows;                            // [row] sum
-  float* s_m = s_l + kRows;                                 // [row] max
-  float4* s_o = reinterpret_cast<float4*>(s_m + kRows);     // [lane of parts][piece]
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int items = heads * kPieces;
-  const int lanes = items < kThreads ? kThreads / items : 1;
-  const int r = lanes > 1 ? tid / items : 0;
-  const int it0 = lanes > 1 ? tid % items : tid;
-  auto row = [&](int p, int it) {
-    return reinterpret_cast<const float4*>(a.part_o + part_slot(c0, p0 + p * step) * kRows * D) + it;
-  };
-  float4 pre[kPre];
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, int c0, int p0, int step, int n, int heads, T* out) {
+  constexpr int V = D / 32;    // values of a lane
+  constexpr int kPre = 16;
+  using P = Pack<float, V>;
+  const int lane = threadIdx.x % 32;
+  for (int i = threadIdx.x / 32; i < heads; i += kWarps) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + i;
+    P* rows = reinterpret_cast<P*>(a.part_o) + i * 32 + lane;
+    const long long mine = part_slot(c0, p0 + min(lane, n - 1) * step) * kRows;
+    const float2 x = __ldcg(ml + mine);
+    float acc[V] = {};
+    P y[kPre];
 #pragma unroll
-  for (int k = 0; k < kPre; ++k) {
-    const int p = r + k * lanes;
-    pre[k] = r < lanes && it0 < items && p < n ? __ldcg(row(p, it0)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int i = warp; i < heads; i += kWarps) {
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (part_slot(c0, p0 + lane * step) * kRows + i) * 2));
-    float top = ml.x;
+    for (int k = 0; k < kPre; ++k)
+      if (k < n) y[k] = load_cg(rows + part_slot(c0, p0 + k * step) * kRows * 32);
+    const float m = lane < n ? x.x : -INFINITY;
+    float top = m;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float f = ex2_approx(ml.x - (top == -INFINITY ? 0.f : top));
-    float sum = f * ml.y;
+    const float f = ex2_approx(m - (top == -INFINITY ? 0.f : top));
+    float sum = lane < n ? f * x.y : 0.f;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    s_f[lane * kRows + i] = f;
-    if (lane == 0) {
-      s_l[i] = sum;
-      s_m[i] = top;
-    }
-  }
-  __syncthreads();
-  for (int it = it0; it < items; it += kThreads) {
-    const int i = it / kPieces;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4& x, int p) {
-      const float f = s_f[p * kRows + i];
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
-    };
-    if (r < lanes) {
-      for (int p = r; p < n; p += kPre * lanes) {
-        float4 x[kPre];
+    for (int k0 = 0; k0 < n; k0 += kPre) {
 #pragma unroll
-        for (int k = 0; k < kPre; ++k)
-          if (p + k * lanes < n) x[k] = it == it0 && p == r ? pre[k] : __ldcg(row(p + k * lanes, it));
+      for (int k = 0; k < kPre; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) % 32);
+        if (k0 + k < n)
 #pragma unroll
-        for (int k = 0; k < kPre; ++k)
-          if (p + k * lanes < n) add(x[k], p + k * lanes);
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(w, y[k].get(e), acc[e]);
       }
+#pragma unroll
+      for (int k = 0; k < kPre; ++k)
+        if (k0 + kPre + k < n) y[k] = load_cg(rows + part_slot(c0, p0 + (k0 + kPre + k) * step) * kRows * 32);
     }
-    if (lanes > 1) {   // uniform: every thread is here once
-      s_o[tid] = acc;
-      __syncthreads();
-      if (r == 0) {
-        for (int k = 1; k < lanes; ++k) {
-          const float4 x = s_o[k * items + it];
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
-        }
-      }
-    }
-    if (r != 0) continue;
     if (out) {
-      const float sum = s_l[i];
       const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
-      *reinterpret_cast<uint2*>(out + it * 4) =
-          make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+      uint32_t* to = reinterpret_cast<uint32_t*>(out + i * D + lane * V);
+#pragma unroll
+      for (int e = 0; e < V; e += 2) to[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
     } else {
-      *const_cast<float4*>(row(0, it)) = acc;
-      if (it % kPieces == 0)
-        *reinterpret_cast<float2*>(a.part_ml + (part_slot(c0, p0) * kRows + i) * 2) = make_float2(s_m[i], s_l[i]);
+      P r;
+#pragma unroll
+      for (int e = 0; e < V; e += 2) r.set2(e / 2, acc[e], acc[e + 1]);
+      const long long at = part_slot(c0, p0) * kRows;
+      rows[at * 32] = r;
+      if (lane == 0) reinterpret_cast<float2*>(a.part_ml)[at + i] = make_float2(top, sum);
     }
   }
 }
@@ -297,46 +331,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   constexpr int kRows = M::kRows;
   constexpr bool kFP16 = kIsFp16<T>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[kWarps];
-  __shared__ long long s_base;
-  __shared__ int s_seq;
-  __shared__ bool s_last;
+  __shared__ Part s_part[2];
+  __shared__ bool s_last[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int units = a.c.H * a.head_groups;   // of a sequence
+  const uint32_t units = a.c.H * a.head_groups;   // of a sequence
 
   pdl_wait();      // the pool, the tables and the queries may come from earlier kernels
   pdl_trigger();
 
-  // The line's length, and where this CTA's part starts.
-  uint32_t magic = 0;
-  if (tid == 0) magic = __ldcg(a.ws_magic);
-  if (tid == 0) s_seq = a.c.n_seqs;
-  auto tiles_at = [&](int s) { return s < a.c.n_seqs ? (long long)seq_tiles<S::kTileTokens>(a, s) * units : 0; };
-  long long total = 0, mine = tiles_at(tid), upto;
-  if (a.c.n_seqs > kThreads) {   // more than a round: the sum of all first
-    long long sum = mine;
-    for (int s = tid + kThreads; s < a.c.n_seqs; s += kThreads) sum += tiles_at(s);
-    block_scan(sum, s_scan, total);
-  }
-  long long round;
-  upto = block_scan(mine, s_scan, round);
-  if (a.c.n_seqs <= kThreads) total = round;
-  const long long parts = total < a.grid ? total : a.grid;
-  Line work;
-  work.t = parts ? blockIdx.x * total / parts : 0;
-  work.end = blockIdx.x < parts ? (blockIdx.x + 1) * total / parts : work.t;
-  for (int s0 = 0;;) {
-    if (mine > 0 && work.t < upto && work.t >= upto - mine) {
-      s_seq = s0 + tid;
-      s_base = upto - mine;
-    }
-    s0 += kThreads;
-    if (s0 >= a.c.n_seqs || work.t < round) break;
-    mine = tiles_at(s0 + tid);
-    const long long before = round;
-    upto = before + block_scan(mine, s_scan, round);
-    round += before;
-  }
+  Split work = split(a, units);
   T* out = static_cast<T*>(a.out);
   const int q_heads = a.c.H * a.group;
   for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x) {
@@ -345,9 +348,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       for (int i = tid; i < q_heads * D; i += kThreads) out[(long long)s * q_heads * D + i] = from_f32<T>(0.f);
   }
   if (work.t >= work.end) return;
-  __syncthreads();
-  work.seq = s_seq;
-  work.base = s_base;
 
   uint8_t* ring = smem + warp * (S::kStages * 2 * S::kHalf);
   const uint32_t ring_u = smem_u32(ring);
@@ -357,115 +357,144 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   // The loads' side runs kStages - 1 steps ahead of the products', over the
   // ends of units. Step i of a warp in a piece: tokens
   // [tok0 + (i kWarps + warp) kStep, + kStep).
-  Line ahead = work;
-  int l_seq = 0, l_head = 0, l_len = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
+  Split ahead = work;
+  constexpr int kPerPass = 32 / S::kChunks;   // rows of a pass
+  const int chunk = lane % S::kChunks;
+  const long long row_size = (long long)a.c.H * D;
+  int l_seq = 0, l_len = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
+  const T* l_src = nullptr;                                       // the lane's chunk of the unit's head in row 0
+  int l_row = -1;                                                 // the lane's row of the next step, looked up ahead
+  bool l_ok = false;
+  auto look_up = [&]() {   // goes on to the next piece where this one has no step left
+    while (l_next >= l_end) {
+      Piece p;
+      if (!next_piece(a, units, ahead, p)) {
+        l_next = INT_MAX;
+        return;
+      }
+      l_seq = p.seq;
+      l_src = pool + p.unit / a.head_groups * D + chunk * 8;
+      l_len = p.len;
+      l_end = p.tok1;
+      l_next = p.tok0 + warp * S::kStep;   // a piece may have no step for this warp
+    }
+    l_row = -1;
+    l_ok = lane < S::kStep && lane < l_end - l_next;
+    if (l_ok) l_row = token_row(a.c, l_seq, l_next + lane);
+  };
   // Requests the next step's rows; bit r of the result is set where row r is
   // a token to attend to.
   auto issue = [&]() -> uint32_t {
-    while (l_next >= l_end) {
-      Piece p;
-      if (!next_piece<S::kTileTokens>(a, units, ahead, p)) return 0;
-      l_seq = p.seq;
-      l_head = p.unit / a.head_groups;
-      l_len = p.len;
-      l_end = p.tile1 == p.tiles ? p.len : p.first + p.tile1 * S::kTileTokens;
-      // a piece's last tile may have no token for this warp
-      const long long from = (long long)p.first + (long long)p.tile0 * S::kTileTokens + warp * S::kStep;
-      l_next = from < l_end ? (int)from : l_end;
-    }
-    int row = -1;
-    bool ok = false;
-    if (lane < S::kStep && lane < l_end - l_next) {
-      const int j = l_next + lane;
-      row = token_row(a.c, l_seq, j);
-      ok = row >= 0;
-      if (!ok) raise_error(a.c.error, kErrIndex);
-      if (kFused && j == l_len - 1) row = -1;   // the new token comes from shared memory
-    }
-    const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-    constexpr int kPerPass = 32 / S::kChunks;   // rows of a pass
-    const int chunk = lane % S::kChunks;
+    if (l_next == INT_MAX) return 0;
+    if (l_ok && l_row < 0) raise_error(a.c.error, kErrIndex);
+    const uint32_t valid = __ballot_sync(0xffffffffu, l_row >= 0);
+    if (kFused && l_next + lane == l_len - 1) l_row = -1;   // the new token comes from shared memory
     const uint32_t dst0 = ring_u + l_stage * (2 * S::kHalf);
 #pragma unroll
     for (int r0 = 0; r0 < S::kStep; r0 += kPerPass) {
       const int r = r0 + lane / S::kChunks;
-      const int from = __shfl_sync(0xffffffffu, row, r);
-      const T* src = pool + row_offset(a.c, from < 0 ? 0 : from, l_head) + chunk * 8;
+      const int from = __shfl_sync(0xffffffffu, l_row, r);
+      const T* src = l_src + max(from, 0) * row_size;
       const uint32_t dst = dst0 + r * (D * 2) + ((chunk ^ (r & 7)) << 4);
       cp_async16(dst, src, from >= 0);
       cp_async16(dst + S::kHalf, src + v_off, from >= 0);
     }
     l_stage = l_stage + 1 == S::kStages ? 0 : l_stage + 1;
-    l_next = l_end - l_next > S::kTileTokens ? l_next + S::kTileTokens : l_end;
+    l_next += S::kStride;
+    look_up();
     return valid;
   };
-  uint32_t valid[S::kStages];
+  look_up();
+  uint32_t valid[S::kStages];   // of the steps under way, the next one first
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) {
     valid[i] = issue();
     cp_async_commit();
   }
 
-  int stage = 0;
+  // A piece's queries, and its new key and value where it holds the new
+  // token: 16 bytes a thread and round, requested a piece ahead.
+  constexpr int kQ = kRows * S::kChunks / kThreads > 0 ? kRows * S::kChunks / kThreads : 1;
+  uint4 raw[kQ], raw_new = make_uint4(0, 0, 0, 0);
+  int new_page = -1, new_pos = -1;
+  auto request = [&](const Piece& p) {
+    const int h = p.unit / a.head_groups, head0 = p.unit % a.head_groups * kRows;
+    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + (h * a.group + head0) * a.q.head_stride;
+#pragma unroll
+    for (int x = 0; x < kQ; ++x) {
+      const int i = (x * kThreads + tid) / S::kChunks, chunk = tid % S::kChunks;
+      raw[x] = i < kRows && head0 + i < a.group ? *reinterpret_cast<const uint4*>(q + i * a.q.head_stride + chunk * 8)
+                                                : make_uint4(0, 0, 0, 0);
+    }
+    if (kFused) {
+      if (a.positions) new_pos = __ldg(a.positions + p.seq);
+      if (p.tok1 == p.len) {
+        new_page = __ldg(a.c.tables + p.seq * a.c.table_stride + page_of(a.c, p.len - 1));
+        if (tid < 2 * S::kChunks) {
+          const RowsIn& from = tid < S::kChunks ? a.k : a.v;
+          raw_new = *reinterpret_cast<const uint4*>(static_cast<const T*>(from.p) + p.seq * from.token_stride +
+                                                    h * from.head_stride + tid % S::kChunks * 8);
+        }
+      }
+    }
+  };
+
+  // The thread's pair of a head's values, in every piece.
+  int e0 = 0, e1 = 0;
+  const bool on = kFused && rope_pair(a.rope, tid % (D / 2), e0, e1);
+  const uint64_t turn = on ? a.rope.turn[tid % (D / 2)] : 0;
+
+  int stage = 0, n_parts = 0;
   Piece p;
-  while (next_piece<S::kTileTokens>(a, units, work, p)) {
+  bool more = next_piece(a, units, work, p);
+  if (more) request(p);
+  while (more) {
     const int h = p.unit / a.head_groups;
     const int head0 = p.unit % a.head_groups * kRows;                     // within the K/V head's group
     const int heads = a.group - head0 < kRows ? a.group - head0 : kRows;
     const int q0 = h * a.group + head0;
-    const int tok0 = p.first + p.tile0 * S::kTileTokens + warp * S::kStep;
-    const int tok1 = p.tile1 == p.tiles ? p.len : p.first + p.tile1 * S::kTileTokens;
-    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + q0 * a.q.head_stride;
-    const bool has_new = kFused && p.tile1 == p.tiles;   // the new token's row lies in this piece
+    const int tok0 = p.tok0 + warp * S::kStep, tok1 = p.tok1;
+    const bool has_new = kFused && tok1 == p.len;   // the new token's row lies in this piece
+    Piece next;
 
+    __syncthreads();   // the last piece's results have been read
+    uint4* sq = reinterpret_cast<uint4*>(smem + M::kOffO);
+    float* sf = reinterpret_cast<float*>(smem + M::kOffTurned);
+    T* sn = reinterpret_cast<T*>(smem + M::kOffNew);
+#pragma unroll
+    for (int x = 0; x < kQ; ++x)
+      if (x * kThreads + tid < kRows * S::kChunks) sq[x * kThreads + tid] = raw[x];
+    const int row_of_new = row_in(a.c, new_page, p.len - 1);
+    const int pos = a.positions ? new_pos : p.len - 1;
+    if (has_new && tid < 2 * S::kChunks) reinterpret_cast<uint4*>(sn)[tid] = raw_new;
+    more = next_piece(a, units, work, next);
+    if (more) request(next);
     if (kFused) {
-      float* sq = reinterpret_cast<float*>(smem + M::kOffO);
-      T* sn = reinterpret_cast<T*>(smem + M::kOffNew);
-      const int pos = a.positions ? __ldg(a.positions + p.seq) : p.len - 1;
-      int e0, e1;
-      const int pair = tid % (D / 2);
-      const bool on = rope_pair(a.rope, pair, e0, e1);
       float c = 1.f, s = 0.f;
-      if (on) rope_angle(a.rope.turn[pair], pos, a.rope.amplitude, c, s);
-      __syncthreads();   // the last unit's results have been read
-      for (int i = tid / (D / 2); i < kRows; i += kThreads / (D / 2)) {
-        float x = 0.f, y = 0.f;
-        if (i < heads) {
-          x = to_f32(q[i * a.q.head_stride + e0]);
-          y = to_f32(q[i * a.q.head_stride + e1]);
-          if (on) rope_turn(x, y, c, s);
-        }
-        sq[i * D + e0] = x;
-        sq[i * D + e1] = y;
-      }
-      if (has_new) {
-        const int row = token_row(a.c, p.seq, p.len - 1);
-        T* to = static_cast<T*>(a.c.pool) + row_offset(a.c, row < 0 ? 0 : row, h);
-        const bool write = row >= 0 && head0 == 0;   // one of the head's groups writes it
-        if (tid < D / 2) {
-          const T* k = static_cast<const T*>(a.k.p) + p.seq * a.k.token_stride + h * a.k.head_stride;
-          T kx = k[e0], ky = k[e1];
-          if (on) {
-            float x = to_f32(kx), y = to_f32(ky);
-            rope_turn(x, y, c, s);
-            kx = from_f32<T>(x);   // the cache's type: attended to as later tokens will read it
-            ky = from_f32<T>(y);
-          }
-          sn[e0] = kx;
-          sn[e1] = ky;
-          if (write) {
-            to[e0] = kx;
-            to[e1] = ky;
-          }
-        }
-        const T* v = static_cast<const T*>(a.v.p) + p.seq * a.v.token_stride + h * a.v.head_stride;
-        for (int i = tid; i < D; i += kThreads) {
-          const T x = v[i];
-          sn[D + i] = x;
-          if (write) to[v_off + i] = x;
-        }
-      }
+      if (on) rope_angle(turn, pos, a.rope.amplitude, c, s);
       __syncthreads();
+      const T* raw_q = reinterpret_cast<const T*>(sq);
+      for (int i = tid / (D / 2); i < kRows; i += kThreads / (D / 2)) {
+        float x = to_f32(raw_q[i * D + e0]), y = to_f32(raw_q[i * D + e1]);
+        if (on) rope_turn(x, y, c, s);
+        sf[i * D + e0] = x;
+        sf[i * D + e1] = y;
+      }
+      if (has_new && on && tid < D / 2) {
+        float x = to_f32(sn[e0]), y = to_f32(sn[e1]);
+        rope_turn(x, y, c, s);
+        sn[e0] = from_f32<T>(x);   // the cache's type: attended to as later tokens will read it
+        sn[e1] = from_f32<T>(y);
+      }
+    }
+    __syncthreads();
+    if (has_new && tid < 2 * S::kChunks) {
+      if (row_of_new < 0) {
+        if (tid == 0) raise_error(a.c.error, kErrIndex);
+      } else if (head0 == 0) {   // one of the head's groups writes it
+        T* to = static_cast<T*>(a.c.pool) + row_offset(a.c, row_of_new, h) + (tid < S::kChunks ? 0 : v_off);
+        reinterpret_cast<uint4*>(to)[tid % S::kChunks] = reinterpret_cast<const uint4*>(sn)[tid];
+      }
     }
 
     // Queries as B operands: heads lane / 4 of each block of 8, values
@@ -477,12 +506,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = n * 8 + lane / 4, d = k * 16 + e * 8 + lane % 4 * 2;
+          const int at = (n * 8 + lane / 4) * D + k * 16 + e * 8 + lane % 4 * 2;
           if (kFused) {
-            const float2 x = *reinterpret_cast<const float2*>(smem + M::kOffO + (i * D + d) * 4);
+            const float2 x = *reinterpret_cast<const float2*>(sf + at);
             split2<T>(x.x, x.y, qb[n][k][e], qlo[n][k][e]);   // the rotated query is not rounded
           } else {
-            qb[n][k][e] = i < heads ? *reinterpret_cast<const uint32_t*>(q + i * a.q.head_stride + d) : 0u;
+            qb[n][k][e] = reinterpret_cast<const uint32_t*>(sq)[at / 2];
           }
         }
 
@@ -491,18 +520,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
 
-    const int n_steps = tok0 < tok1 ? (tok1 - tok0 + S::kTileTokens - 1) / S::kTileTokens : 0;
+    const int n_steps = tok0 < tok1 ? (tok1 - tok0 + S::kStride - 1) / S::kStride : 0;
     for (int i = 0; i < n_steps; ++i) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();
       valid[S::kStages - 1] = issue();
       cp_async_commit();
-      const uint32_t on = valid[0];
+      const uint32_t seen = valid[0];
 #pragma unroll
       for (int k = 0; k < S::kStages - 1; ++k) valid[k] = valid[k + 1];
       const uint32_t ks = ring_u + stage * (2 * S::kHalf), vs = ks + S::kHalf;
       if (kFused && has_new) {
-        const int r = p.len - 1 - (tok0 + i * S::kTileTokens);
+        const int r = p.len - 1 - (tok0 + i * S::kStride);
         if (r >= 0 && r < S::kStep) {
           if (lane < 2 * S::kChunks) {
             const int chunk = lane % S::kChunks;
@@ -516,12 +545,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
       // S^T: rows are tokens lane / 4 and lane / 4 + 8 of each block, columns
-      // heads (lane % 4) * 2 and the next.
+      // heads (lane % 4) * 2 and the next. Even and odd products (and the
+      // queries' remainders) in sums of their own: shorter chains.
+      constexpr int kSums = kFused ? 4 : 2;
       float sc[S::kM][NT][4];
 #pragma unroll
       for (int b = 0; b < S::kM; ++b) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[b][n][0] = sc[b][n][1] = sc[b][n][2] = sc[b][n][3] = 0.f;
+        float part[NT][kSums][4] = {};
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t x[4];
@@ -529,44 +559,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
           ldsm_x4(ks + r * (D * 2) + (((2 * k + lane / 16) ^ (r & 7)) << 4), x);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_16816<kFP16>(sc[b][n], x, qb[n][k][0], qb[n][k][1]);
-            if (kFused) mma_16816<kFP16>(sc[b][n], x, qlo[n][k][0], qlo[n][k][1]);
+            mma_16816<kFP16>(part[n][k % 2], x, qb[n][k][0], qb[n][k][1]);
+            if (kFused) mma_16816<kFP16>(part[n][2 + k % 2], x, qlo[n][k][0], qlo[n][k][1]);
           }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = part[n][0][e] + part[n][1][e];
+            if constexpr (kFused) x += part[n][2][e] + part[n][3][e];
+            sc[b][n][e] = x * a.scale_log2;
+          }
       }
       constexpr uint32_t kAll = S::kStep == 32 ? 0xffffffffu : (1u << S::kStep % 32) - 1;
-      float top[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        top[n][0] = top[n][1] = -INFINITY;
+      if (seen != kAll) {
 #pragma unroll
         for (int b = 0; b < S::kM; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = b * 16 + lane / 4 + (e >> 1) * 8;
-            const float x = sc[b][n][e] * a.scale_log2;
-            sc[b][n][e] = on == kAll || (on >> r & 1) ? x : -INFINITY;
-            top[n][e & 1] = fmaxf(top[n][e & 1], sc[b][n][e]);
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(seen >> (b * 16 + lane / 4 + (e >> 1) * 8) & 1)) sc[b][n][e] = -INFINITY;
       }
+      // The reference m follows the scores' maximum only when one exceeds it
+      // by kSlack (a power of two: p stays below 2^kSlack, and O and l have
+      // the same factor). Mostly a vote is all it takes.
+      float top[NT][2];
       bool grew = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x = top[n][c];
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          top[n][c] = fmaxf(x, m[n][c]);
-          grew |= top[n][c] > m[n][c];
+          top[n][c] = fmaxf(sc[0][n][c], sc[0][n][c + 2]);
+          if constexpr (S::kM == 2) top[n][c] = fmaxf(top[n][c], fmaxf(sc[1][n][c], sc[1][n][c + 2]));
+          grew |= top[n][c] > m[n][c] + kSlack;
         }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float f = top[n][c] > m[n][c] ? ex2_approx(m[n][c] - top[n][c]) : 1.f;   // 0 from -inf
-            m[n][c] = top[n][c];
+            float x = top[n][c];
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float f = x > m[n][c] ? ex2_approx(m[n][c] - x) : 1.f;   // 0 from -inf
+            m[n][c] = fmaxf(x, m[n][c]);
             l[n][c] *= f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -616,9 +654,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     // Join the warps in shared memory, a block of 8 heads at a time.
     float* wo = reinterpret_cast<float*>(smem + M::kOffO);
     float* wml = reinterpret_cast<float*>(smem + M::kOffMl);
-    const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
-    const int c0 = whole ? 0 : (int)(((p.unit_base + 1) * parts - 1) / total);   // the unit's first CTA
-    const long long slot = part_slot(c0, blockIdx.x - c0);
+    const bool whole = p.parts == 1;
+    const long long slot = part_slot(p.c0, blockIdx.x - p.c0);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n > 0 && heads <= n * 8) break;
@@ -664,38 +701,65 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         }
       }
     }
-    if (!whole) {
-      // The parts of the unit, this CTA's among them; the last to arrive joins.
-      const int n = (int)(((p.unit_base + p.tiles) * parts - 1) / total) - c0 + 1;
-      const int me = blockIdx.x - c0;
-      T* to = out + ((long long)p.seq * q_heads + q0) * D;
-      const bool two = n > kJoin;
-      const int g0 = two ? me / kGroup * kGroup : 0;
-      const int of = two ? min(kGroup, n - g0) : n;
-      __syncthreads();
-      if (tid == 0) {
-        if (magic != kWorkspaceMagic) raise_error(a.c.error, kErrWorkspace);
-        s_last = magic == kWorkspaceMagic && arrive_last(a.counters + part_slot(c0, g0), of);
-      }
-      __syncthreads();
-      if (s_last) {
-        join_parts<D, T, kRows>(a, wo, c0, g0, 1, of, heads, two ? nullptr : to);
-        if (two) {
-          const int groups = (n + kGroup - 1) / kGroup;
-          __syncthreads();
-          if (tid == 0) s_last = arrive_last(a.counters + 2 * a.grid + part_slot(c0, 0), groups);
-          __syncthreads();
-          if (s_last) join_parts<D, T, kRows>(a, wo, c0, 0, kGroup, groups, heads, to);
-        }
-      }
+    if (!whole) {   // its unit is joined at the CTA's end: an arrival takes microseconds while the memory is busy
+      if (tid == 0) s_part[n_parts] = {p.c0, p.parts, heads, p.seq * q_heads + q0};
+      ++n_parts;
     }
+    p = next;
   }
   cp_async_wait<0>();
+
+  // The CTA's parts of split units, two at most: its first piece and its
+  // last. Of each unit the last part to arrive joins.
+  for (int round = 0; round < 2; ++round) {
+    __syncthreads();
+    if (lane == 0 && warp < n_parts) {
+      const Part x = s_part[warp];
+      const bool two = x.parts > kJoin;
+      const int me = blockIdx.x - x.c0, g0 = two ? me / kGroup * kGroup : 0;
+      bool last = false;
+      if (round == 0) {
+        if (*a.ws_magic == kWorkspaceMagic)
+          last = arrive_last(a.counters + part_slot(x.c0, g0), two ? min(kGroup, x.parts - g0) : x.parts);
+        else
+          raise_error(a.c.error, kErrWorkspace);
+      } else if (two && s_last[warp]) {
+        last = arrive_last(a.counters + 2 * a.grid + part_slot(x.c0, 0), (x.parts + kGroup - 1) / kGroup);
+      }
+      s_last[warp] = last;
+    }
+    __syncthreads();
+    bool again = false;
+    for (int i = 0; i < n_parts; ++i) {
+      if (!s_last[i]) continue;
+      const Part x = s_part[i];
+      T* to = out + (long long)x.row * D;
+      if (x.parts <= kJoin) {
+        join_parts<D, T, kRows>(a, x.c0, 0, 1, x.parts, x.heads, to);
+      } else if (round == 0) {
+        const int g0 = (blockIdx.x - x.c0) / kGroup * kGroup;
+        join_parts<D, T, kRows>(a, x.c0, g0, 1, min(kGroup, x.parts - g0), x.heads, nullptr);
+        again = true;
+      } else {
+        join_parts<D, T, kRows>(a, x.c0, 0, kGroup, (x.parts + kGroup - 1) / kGroup, x.heads, to);
+      }
+    }
+    if (!again) break;   // uniform
+  }
 }
 
 int decode_rows(int group) { return group <= 8 ? 8 : 16; }
 
 int decode_grid(int num_sms) { return num_sms * kCtasPerSm; }
+
+// log2 of the tokens of a tile: the finest that keeps the line of the longest
+// possible sequences, every unit's cost included, within 31 bits.
+int decode_tile_shift(int D, int n_seqs, int units, long long most_tokens) {
+  int shift = D == 64 ? 7 : 6;
+  static_assert(Shape<64>::kStride == 128 && Shape<128>::kStride == 64, "the finest tile is a step of all warps");
+  while (((most_tokens >> shift) + 1 + kUnitCost) * n_seqs * units > INT_MAX && shift < 30) ++shift;
+  return shift;
+}
 
 template <int D, typename T, int NT, bool kFused>
 static cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {

@@ -70,6 +70,16 @@ struct Pack<T, 1> {
   __device__ __forceinline__ void set(float a) { v = from_f32<T>(a); }
 };
 
+// Past the first-level cache: written by other CTAs of the launch.
+__device__ __forceinline__ Pack<float, 2> load_cg(const Pack<float, 2>* p) {
+  const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
+  return {{x.x, x.y}};
+}
+__device__ __forceinline__ Pack<float, 4> load_cg(const Pack<float, 4>* p) {
+  const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p));
+  return {{x.x, x.y, x.z, x.w}};
+}
+
 // Bits of the cache's error word (kv_tokens_check).
 constexpr uint32_t kErrIndex = 2u;       // a page id, a length or cu_new out of range
 constexpr uint32_t kErrWorkspace = 4u;   // a workspace that was not prepared
@@ -77,11 +87,11 @@ constexpr uint32_t kErrWorkspace = 4u;   // a workspace that was not prepared
 __device__ __forceinline__ void raise_error(uint32_t* word, uint32_t bit) { atomicOr(word, bit); }
 
 // The length of sequence s, held to what its table can name.
-__device__ __forceinline__ int seq_len(const TokenCache& c, int s) {
-  const int n = __ldg(c.lens + s);
+__device__ __forceinline__ int held(const TokenCache& c, int n) {
   const int most = c.table_width * c.page_size;   // <= 2^30, checked by the host
   return n < 0 ? 0 : n > most ? most : n;
 }
+__device__ __forceinline__ int seq_len(const TokenCache& c, int s) { return held(c, __ldg(c.lens + s)); }
 __device__ __forceinline__ bool seq_len_bad(const TokenCache& c, int s) {
   const int n = __ldg(c.lens + s);
   return n < 0 || n > c.table_width * c.page_size;
@@ -93,14 +103,15 @@ __device__ __forceinline__ int divided(int j, uint32_t mul, int shift) {
 }
 __device__ __forceinline__ int page_of(const TokenCache& c, int j) { return divided(j, c.page_mul, c.page_shift); }
 
-// K row of token j of sequence s in the pool's [max_pages * 2 * page_size]
-// rows (its V row is page_size further), or -1 where the table holds no page
-// of the pool. Rows fit 31 bits (checked by the host).
-__device__ __forceinline__ int token_row(const TokenCache& c, int s, int j) {
-  const int i = page_of(c, j);
-  const int page = __ldg(c.tables + s * c.table_stride + i);
+// K row of the sequence's token j, on page `page`, in the pool's
+// [max_pages * 2 * page_size] rows (its V row is page_size further), or -1
+// where that is no page of the pool. Rows fit 31 bits (checked by the host).
+__device__ __forceinline__ int row_in(const TokenCache& c, int page, int j) {
   if ((unsigned)page >= (unsigned)c.max_pages) return -1;
-  return page * 2 * c.page_size + (j - i * c.page_size);
+  return page * 2 * c.page_size + (j - page_of(c, j) * c.page_size);
+}
+__device__ __forceinline__ int token_row(const TokenCache& c, int s, int j) {
+  return row_in(c, __ldg(c.tables + s * c.table_stride + page_of(c, j)), j);
 }
 
 // Head h of token row `row`: offset in elements.

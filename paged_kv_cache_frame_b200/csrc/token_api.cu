@@ -107,8 +107,7 @@ DecodeLayout decode_layout(int D, int group) {
 }
 
 int check_group(const kv_tokens* c, int q_heads, const std::string& who) {
-  // With KV_MAX_TOKEN_SEQS and 2^30 tokens a sequence the bound keeps the
-  // kernels' products of tiles and CTAs within 63 bits.
+  // With KV_MAX_TOKEN_SEQS the bound leaves the units' count below 2^27.
   if (q_heads < 1 || q_heads > KV_MAX_Q_HEADS || q_heads % c->num_heads != 0)
     return api_fail(KV_ERR_ARG, who + ": q_heads must be a multiple of the pool's heads, at most KV_MAX_Q_HEADS");
   return KV_OK;
@@ -147,6 +146,8 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   a.head_groups = (a.group + rows - 1) / rows;
   a.window = window;
   a.grid = l.grid;
+  a.tile_shift = pkv::decode_tile_shift(c->head_dim, c->n_seqs, c->num_heads * a.head_groups,
+                                        (long long)c->table_width * c->page_size);
   const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
   a.scale_log2 = (float)(s * 1.4426950408889634);
   const cudaError_t e = pkv::launch_decode(a, c->dtype, fused, (cudaStream_t)stream);

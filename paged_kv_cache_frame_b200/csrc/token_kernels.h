@@ -72,6 +72,7 @@ struct DecodeArgs {
   int head_groups;            // groups of at most `rows` query heads a unit takes
   int window;                 // 0: the whole cache
   int grid;                   // CTAs of the attention launch
+  int tile_shift;             // log2 of a tile's tokens
   float scale_log2;           // scale * log2(e)
   RopeTable rope;
 };
@@ -81,6 +82,7 @@ cudaError_t launch_append_tokens(const AppendTokensArgs& a, int dtype, cudaStrea
 // Query heads one unit takes (8 or 16) and CTAs of a launch.
 int decode_rows(int group);
 int decode_grid(int num_sms);
+int decode_tile_shift(int D, int n_seqs, int units, long long most_tokens);
 cudaError_t launch_decode(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
 
 }  // namespace pkv

@@ -266,68 +266,84 @@ def test_sequence_search():
         assert 0 <= find_seq(cu, n, rng.randint(0, 50)) <= n
 
 
-JOIN, GROUP = 32, 16   # parts joined in one round, and neighbours joined first where there are more
+JOIN, GROUP = 32, 16      # parts joined in one round, and neighbours joined first where there are more
+PART, COST = 3, 3         # tiles a part holds at most, a unit's own cost in the line
 
 
-def line_pieces(tiles, units, grid):
-    """The pieces of every CTA as the attention kernel cuts the line: unit
-    key, CTA, tiles, and of a split unit its slot, first CTA and parts."""
-    total = sum(t * units for t in tiles)
-    parts = min(grid, total)
+def split_pieces(tiles, units, grid):
+    """The pieces of every CTA as the attention kernel splits them: unit key,
+    CTA, tiles, the unit's first CTA and its parts."""
+    parts_of = lambda n: (n + PART - 1) // PART  # noqa: E731
+    n_parts = sum(parts_of(n) * units for n in tiles)
+    by_parts = n_parts <= grid
+    total = sum((n + COST) * units for n in tiles if n)
+    each, more = divmod(total, grid)
+
+    def cta_of(place):
+        lower = more * (each + 1)
+        return place // (each + 1) if place < lower else more + (place - lower) // each
+
     pieces = []
-    for c in range(parts):
-        t, end, base, seq = c * total // parts, (c + 1) * total // parts, 0, 0
+    for c in range(grid):
+        if by_parts:
+            t, end = min(c, n_parts), min(c + 1, n_parts)
+        else:
+            t = c * each + min(c, more)
+            end = t + each + (c < more)
+        base, seq = 0, 0
         while t < end:
-            while t >= base + tiles[seq] * units:
-                base += tiles[seq] * units
+            while True:
+                n = tiles[seq]
+                size = parts_of(n) if by_parts else n + COST if n else 0
+                if t - base < size * units:
+                    break
+                base += size * units
                 seq += 1
-            n = tiles[seq]
-            unit = (t - base) // n
-            unit_base = base + unit * n
-            t0 = t - unit_base
-            t1 = n if n - t0 < end - t else t0 + end - t
-            split = None
-            if t0 > 0 or t1 < n:
-                c0 = ((unit_base + 1) * parts - 1) // total
-                split = (2 * c + (1 if c == c0 else 0), c0, ((unit_base + n) * parts - 1) // total - c0 + 1)
-            pieces.append(((seq, unit), c, t0, t1, split))
-            t += t1 - t0
+            unit, at = divmod(t - base, size)
+            if by_parts:
+                t0, t1 = n * at // size, n * (at + 1) // size
+                c0, parts = t - at, size
+                t += 1
+            else:
+                took = min(end - t, size - at)
+                t0, t1 = max(0, at - COST), max(0, at + took - COST)
+                first = t - at
+                c0 = cta_of(first + COST)
+                parts = cta_of(first + size - 1) - c0 + 1
+                t += took
+            if t0 < t1:
+                pieces.append(((seq, unit), c, t0, t1, c0, parts))
     return pieces
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(120))
 def test_split_covers_every_tile_and_the_join_finds_the_parts(seed):
-    """Every tile once; a unit's parts in the slots the join reads; arrivals
-    counted to the number that comes, on counters no two units share."""
+    """Every tile once; a unit's parts in neighbouring CTAs and slots no other
+    part has; arrivals counted to the number that comes, on counters no two
+    units share."""
     rng = random.Random(seed)
     seqs, units, grid = rng.choice([1, 2, 7, 64, 300]), rng.choice([1, 2, 8, 24]), rng.choice([1, 4, 296])
-    tiles = [rng.choice([0, 1, 2, 5, rng.randint(0, 400)]) for _ in range(seqs)]
-    if not sum(tiles):
-        tiles[-1] = 1
-    pieces = line_pieces(tiles, units, grid)
+    most = rng.choice([3, 20, 400, 9000])
+    tiles = [rng.choice([0, 1, 2, 5, rng.randint(0, most)]) for _ in range(seqs)]
+    pieces = split_pieces(tiles, units, grid)
     assert set(k for k, *_ in pieces) == {(s, u) for s in range(seqs) if tiles[s] for u in range(units)}
     by_unit, slots, first, second = {}, set(), {}, {}
-    for key, c, t0, t1, split in pieces:
-        by_unit.setdefault(key, []).append((t0, t1, c, split))
-        if split:
-            slot, c0, n = split
+    for key, c, t0, t1, c0, n in pieces:
+        by_unit.setdefault(key, []).append((t0, t1, c, c0, n))
+        if n > 1:
+            slot = 2 * c + (c == c0)
             assert slot < 2 * grid and slot not in slots
             slots.add(slot)
             two, me = n > JOIN, c - c0
             g0 = me // GROUP * GROUP if two else 0
-            counter = 2 * (c0 + g0) + (1 if g0 == 0 else 0)
-            of = min(GROUP, n - g0) if two else n
-            first.setdefault(counter, []).append((key, of))
+            counter = 2 * (c0 + g0) + (g0 == 0)
+            first.setdefault(counter, []).append((key, min(GROUP, n - g0) if two else n))
             if two and me == g0:
                 second.setdefault(2 * c0 + 1, []).append((key, (n + GROUP - 1) // GROUP))
     for counters in (first, second):
         for arrivals in counters.values():
             assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][1] <= JOIN
     for (seq, _), p in by_unit.items():
-        p.sort(key=lambda x: x[:3])
+        p.sort()
         assert p[0][0] == 0 and p[-1][1] == tiles[seq] and all(a[1] == b[0] for a, b in zip(p, p[1:]))
-        if len(p) > 1:
-            c0 = p[0][2]
-            assert [x[3] for x in p] == [(2 * (c0 + i) + (1 if i == 0 else 0), c0, len(p)) for i in range(len(p))]
-        else:
-            assert p[0][3] is None
+        assert [x[2:] for x in p] == [(p[0][3] + i, p[0][3], len(p)) for i in range(len(p))]
