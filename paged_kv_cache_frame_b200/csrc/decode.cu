@@ -105,6 +105,8 @@ struct Smem {
   static constexpr int kBytes = kOffNew + 2 * D * 2;
   static constexpr int kOffTurned = kOffO + kRows * D * 2;             // queries [row][D] fp32, behind them as they came
   static_assert(kRows * D * 6 <= kWarps * 8 * D * 4, "the queries fit the warps' O");
+  // An SM has 228 KB, of which every CTA takes 1 KB and its static part besides.
+  static_assert(kCtasPerSm * (kBytes + 1024 + 128) <= 228 * 1024, "the CTAs of an SM fit");
 };
 
 // Element d of row i of a warp's O block: row i shifted by 4 i floats, so
@@ -134,8 +136,9 @@ struct Split {
   bool by_parts;      // a part a CTA; else the line
   uint32_t each, more;   // the line: CTAs below `more` take each + 1 places, the others `each`
   uint32_t t, end;    // places [t, end) of the line (or parts of all units) are left
-  uint32_t base;      // the first place of sequence seq
+  // Where place t lies: sequence, unit, place `at` of the unit's `size`.
   int seq;
+  uint32_t unit, at, size, tiles;
   int len, later;     // the lengths of seq and seq + 1: read a sequence ahead, as a load takes
                       // about a microsecond while the memory is busy
 
@@ -158,42 +161,54 @@ __device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
 }
 __device__ __forceinline__ uint32_t parts_of(uint32_t tiles) { return (tiles + kPartTiles - 1) / kPartTiles; }
 
+// The places of a unit of the split's current sequence.
+__device__ __forceinline__ void measure(const DecodeArgs& a, Split& l) {
+  l.tiles = tiles_of(a, l.len);
+  l.size = l.by_parts ? parts_of(l.tiles) : l.tiles ? l.tiles + kUnitCost : 0;
+}
+__device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
+  ++l.seq;
+  l.len = held(a.c, l.later);
+  l.later = raw_len(a, l.seq + 1);
+  measure(a, l);
+}
+
 __device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t units, Split& l, Piece& p) {
   while (l.t < l.end) {
-    uint32_t tiles = 0, size = 0;   // places of a unit
-    for (; l.seq < a.c.n_seqs; ++l.seq) {
-      tiles = tiles_of(a, l.len);
-      size = l.by_parts ? parts_of(tiles) : tiles ? tiles + kUnitCost : 0;
-      if (l.t - l.base < size * units) break;
-      l.base += size * units;
-      l.len = held(a.c, l.later);
-      l.later = raw_len(a, l.seq + 2);
+    if (l.at >= l.size) {   // on to the next unit
+      l.at = 0;
+      if (++l.unit >= units || l.size == 0) {
+        l.unit = 0;
+        do next_sequence(a, l);
+        while (l.size == 0 && l.seq < a.c.n_seqs);
+      }
     }
     if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
-    const uint32_t off = l.t - l.base, unit = off / size, at = off - unit * size;
     uint32_t tile0, tile1;
     if (l.by_parts) {
-      tile0 = (uint32_t)((unsigned long long)tiles * at / size);
-      tile1 = (uint32_t)((unsigned long long)tiles * (at + 1) / size);
-      p.c0 = l.t - at;
-      p.parts = size;
+      tile0 = (uint32_t)((unsigned long long)l.tiles * l.at / l.size);
+      tile1 = (uint32_t)((unsigned long long)l.tiles * (l.at + 1) / l.size);
+      p.c0 = l.t - l.at;
+      p.parts = l.size;
       ++l.t;
+      ++l.at;
     } else {
-      const uint32_t n = min(l.end - l.t, size - at);
-      tile0 = at > kUnitCost ? at - kUnitCost : 0;
-      tile1 = at + n > kUnitCost ? at + n - kUnitCost : 0;
-      const uint32_t first = l.t - at;
-      p.c0 = l.cta_of(first + kUnitCost);
-      p.parts = l.cta_of(first + size - 1) - p.c0 + 1;
+      const uint32_t n = min(l.end - l.t, l.size - l.at);
+      const uint32_t first = l.t - l.at;   // the unit's first place; its tiles begin kUnitCost later
+      tile0 = l.at > kUnitCost ? l.at - kUnitCost : 0;
+      tile1 = l.at + n > kUnitCost ? l.at + n - kUnitCost : 0;
+      p.c0 = tile0 == 0 ? blockIdx.x : l.cta_of(first + kUnitCost);
+      p.parts = (tile1 == l.tiles ? blockIdx.x : l.cta_of(first + l.size - 1)) - p.c0 + 1;
       l.t += n;
+      l.at += n;
     }
     if (tile0 == tile1) continue;
     p.seq = l.seq;
-    p.unit = unit;
+    p.unit = l.unit;
     p.len = l.len;
-    const int first = first_seen(a, l.len);
-    p.tok0 = first + (int)(tile0 << a.tile_shift);
-    p.tok1 = tile1 == tiles ? p.len : first + (int)(tile1 << a.tile_shift);
+    const int seen = first_seen(a, l.len);
+    p.tok0 = seen + (int)(tile0 << a.tile_shift);
+    p.tok1 = tile1 == l.tiles ? p.len : seen + (int)(tile1 << a.tile_shift);
     return true;
   }
   return false;
@@ -237,17 +252,22 @@ __device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t units) {
   const uint32_t here = __ballot_sync(0xffffffffu, l.t < last && l.t >= last - size);
   const int owner = here ? __ffs(here) - 1 : 31;
   l.seq = __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner);
-  l.base = __shfl_sync(0xffffffffu, last - size, owner);
-  l.len = held(a.c, raw_len(a, l.seq));
-  l.later = raw_len(a, l.seq + 1);
-  return l;   // next_piece goes on from the stretch's first sequence
+  uint32_t base = __shfl_sync(0xffffffffu, last - size, owner);   // the stretch's first place
+  l.unit = l.at = 0;
+  l.later = raw_len(a, l.seq);
+  --l.seq;
+  for (;;) {   // to the sequence of place t within the stretch
+    next_sequence(a, l);
+    if (l.seq >= a.c.n_seqs || l.t - base < l.size * units) break;
+    base += l.size * units;
+  }
+  if (l.size) {
+    l.unit = (l.t - base) / l.size;
+    l.at = l.t - base - l.unit * l.size;
+  }
+  return l;
 }
 
-// A split unit's part that this CTA holds: the unit's first CTA, its parts,
-// its query heads and the first one's row of `out`.
-struct Part {
-  int c0, parts, heads, row;
-};
 
 // A part of a unit: CTA c0 + p's, in that CTA's second slot if it opened the
 // unit, else in its first.
@@ -273,7 +293,7 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
 template <int D, typename T, int kRows>
 __device__ __forceinline__ void join_parts(const DecodeArgs& a, int c0, int p0, int step, int n, int heads, T* out) {
   constexpr int V = D / 32;    // values of a lane
-  constexpr int kPre = 16;
+  constexpr int kPre = 8; 
   using P = Pack<float, V>;
   const int lane = threadIdx.x % 32;
   for (int i = threadIdx.x / 32; i < heads; i += kWarps) {
@@ -331,8 +351,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   constexpr int kRows = M::kRows;
   constexpr bool kFP16 = kIsFp16<T>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Part s_part[2];
-  __shared__ bool s_last[2];
+  __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t units = a.c.H * a.head_groups;   // of a sequence
 
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   const bool on = kFused && rope_pair(a.rope, tid % (D / 2), e0, e1);
   const uint64_t turn = on ? a.rope.turn[tid % (D / 2)] : 0;
 
-  int stage = 0, n_parts = 0;
+  int stage = 0;
   Piece p;
   bool more = next_piece(a, units, work, p);
   if (more) request(p);
@@ -701,51 +720,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
         }
       }
     }
-    if (!whole) {   // its unit is joined at the CTA's end: an arrival takes microseconds while the memory is busy
-      if (tid == 0) s_part[n_parts] = {p.c0, p.parts, heads, p.seq * q_heads + q0};
-      ++n_parts;
+    if (!whole) {
+      // The parts of the unit, this CTA's among them; the last to arrive joins.
+      T* to = out + ((long long)p.seq * q_heads + q0) * D;
+      const bool two = p.parts > kJoin;
+      const int me = blockIdx.x - p.c0, g0 = two ? me / kGroup * kGroup : 0;
+      const int of = two ? min(kGroup, p.parts - g0) : p.parts;
+      const int groups = (p.parts + kGroup - 1) / kGroup;
+      __syncthreads();
+      if (tid == 0) {
+        const bool ready = *a.ws_magic == kWorkspaceMagic;
+        if (!ready) raise_error(a.c.error, kErrWorkspace);
+        s_last = ready && arrive_last(a.counters + part_slot(p.c0, g0), of);
+      }
+      __syncthreads();
+      bool last = s_last;
+      if (last) join_parts<D, T, kRows>(a, p.c0, g0, 1, of, heads, two ? nullptr : to);
+      if (last && two) {
+        __syncthreads();
+        if (tid == 0) s_last = arrive_last(a.counters + 2 * a.grid + part_slot(p.c0, 0), groups);
+        __syncthreads();
+        last = s_last;
+        if (last) join_parts<D, T, kRows>(a, p.c0, 0, kGroup, groups, heads, to);
+      }
     }
     p = next;
   }
   cp_async_wait<0>();
-
-  // The CTA's parts of split units, two at most: its first piece and its
-  // last. Of each unit the last part to arrive joins.
-  for (int round = 0; round < 2; ++round) {
-    __syncthreads();
-    if (lane == 0 && warp < n_parts) {
-      const Part x = s_part[warp];
-      const bool two = x.parts > kJoin;
-      const int me = blockIdx.x - x.c0, g0 = two ? me / kGroup * kGroup : 0;
-      bool last = false;
-      if (round == 0) {
-        if (*a.ws_magic == kWorkspaceMagic)
-          last = arrive_last(a.counters + part_slot(x.c0, g0), two ? min(kGroup, x.parts - g0) : x.parts);
-        else
-          raise_error(a.c.error, kErrWorkspace);
-      } else if (two && s_last[warp]) {
-        last = arrive_last(a.counters + 2 * a.grid + part_slot(x.c0, 0), (x.parts + kGroup - 1) / kGroup);
-      }
-      s_last[warp] = last;
-    }
-    __syncthreads();
-    bool again = false;
-    for (int i = 0; i < n_parts; ++i) {
-      if (!s_last[i]) continue;
-      const Part x = s_part[i];
-      T* to = out + (long long)x.row * D;
-      if (x.parts <= kJoin) {
-        join_parts<D, T, kRows>(a, x.c0, 0, 1, x.parts, x.heads, to);
-      } else if (round == 0) {
-        const int g0 = (blockIdx.x - x.c0) / kGroup * kGroup;
-        join_parts<D, T, kRows>(a, x.c0, g0, 1, min(kGroup, x.parts - g0), x.heads, nullptr);
-        again = true;
-      } else {
-        join_parts<D, T, kRows>(a, x.c0, 0, kGroup, (x.parts + kGroup - 1) / kGroup, x.heads, to);
-      }
-    }
-    if (!again) break;   // uniform
-  }
 }
 
 int decode_rows(int group) { return group <= 8 ? 8 : 16; }
