@@ -2,12 +2,14 @@
 // way, the values as they are, each row to the page and slot that the
 // sequence's table gives for the token's index.
 //
-// Bound by its bytes. As in the rotation kernel a block takes a few tokens
-// with all of their heads, and its threads go through the (token, head) rows,
-// each at its own unit of V pairs; the values' packs 2u and 2u + 1 travel in
-// the same thread. A warp finds the sequence of a token in cu_new with 32
-// probes at a time (two rounds for up to 1024 sequences) while the first rows
-// are on their way.
+// Bound by its bytes and, short of some ten thousand tokens, by the chain of
+// loads before a row's place is known. As in the rotation kernel a block takes
+// a few tokens with all of their heads, and its threads go through the
+// (token, head) rows, each at its own unit of V pairs; the values' packs 2u
+// and 2u + 1 travel in the same thread. The first rows are on their way
+// meanwhile; cu_new and the lengths are fetched together into shared memory,
+// a thread a token searches there, and only its page is another load. Blocks
+// are made large enough for all of them to run at once.
 #include "launch.cuh"
 #include "rope_unit.cuh"
 
@@ -15,31 +17,31 @@ namespace pkv {
 
 namespace {
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kAhead = 2;         // rows in flight per thread, keys and values
-constexpr int kMaxTokens = 8;     // tokens of a block: one per warp for the search
+constexpr int kMaxTokens = 16;    // tokens of a block
+constexpr int kMaxSeqs = 1024;    // sequences whose cu_new and lengths are kept in shared memory
 
-// Sequences s of [0, n) with cu[s + 1] <= t, all before the others: the
-// sequence of token t (n where no sequence holds it). All lanes of a warp.
+// Sequences of [0, n) that end at or before token t, all before the others:
+// the sequence of token t (n where no sequence holds it).
 __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
-  const int lane = threadIdx.x & 31;
   int lo = 0, hi = n;   // the answer lies in [lo, hi]
   while (lo < hi) {
-    const int step = (hi - lo + 31) / 32;
-    const int probe = lo + (lane + 1) * step - 1;   // the last of the lane's stretch
-    const bool below = probe < hi && __ldg(cu + probe + 1) <= t;
-    const int k = __popc(__ballot_sync(0xffffffffu, below));
-    lo = min(lo + k * step, hi);
-    hi = min(lo + step - 1, hi);
+    const int mid = (lo + hi) / 2;
+    if (cu[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
   }
   return lo;
 }
 }  // namespace
 
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid_constant__ AppendTokensArgs a, int units,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) append_tokens_kernel(const __grid_constant__ AppendTokensArgs a, int units,
                                                                  int per_block) {
   extern __shared__ __align__(16) float2 s_angle[];
   __shared__ int s_row[kMaxTokens];   // pool row of the token's key, -1: not written
+  __shared__ int s_pos[kMaxTokens];
+  __shared__ int s_cu[kMaxSeqs + 1], s_len[kMaxSeqs];
   const int u = threadIdx.x % units;
   const int slot = threadIdx.x / units, slots = kThreads / units;
   const int first = (int)blockIdx.x * per_block;
@@ -66,28 +68,36 @@ __global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid
     }
   };
   load(slot);   // on their way while places and angles are worked out
-  // A warp a token: its row, then its angles.
-  const int lane = threadIdx.x % 32;
-  for (int i = threadIdx.x / 32; i < tokens; i += kThreads / 32) {
-    const int t = first + i;
+  const int n = a.c.n_seqs;
+  const bool kept = a.cu_new && n <= kMaxSeqs;
+  if (kept) {
+    for (int i = threadIdx.x; i <= n; i += kThreads) {
+      s_cu[i] = __ldg(a.cu_new + i);
+      if (i < n) s_len[i] = __ldg(a.c.lens + i);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < tokens) {
+    const int i = threadIdx.x, t = first + i;
+    const int32_t* cu = kept ? s_cu : a.cu_new;
     int s = t, back = 1;   // the token is the back-th from the end of sequence s
-    if (a.cu_new) {
-      s = find_seq(a.cu_new, a.c.n_seqs, t);
+    if (cu) {
+      s = find_seq(cu, n, t);
       // Tokens behind the last sequence belong to none. A cu_new that does not
       // start at 0 or runs backwards can leave t outside of the sequence found.
-      if (s < a.c.n_seqs) {
-        back = __ldg(a.cu_new + s + 1) - t;
-        if (t < __ldg(a.cu_new + s) || back < 1) {
-          s = a.c.n_seqs;
-          if (lane == 0) raise_error(a.c.error, kErrIndex);
+      if (s < n) {
+        back = cu[s + 1] - t;
+        if (t < cu[s] || back < 1) {
+          s = n;
+          raise_error(a.c.error, kErrIndex);
         }
       }
     }
     int at = -1, pos = 0;
-    if (s < a.c.n_seqs) {
-      const int len = seq_len(a.c, s);
+    if (s < n) {
+      const int raw = kept ? s_len[s] : __ldg(a.c.lens + s), len = held(a.c, raw);
       const int j = len - back;
-      bool bad = seq_len_bad(a.c, s);
+      bool bad = raw != len;
       if (j >= 0) {
         at = token_row(a.c, s, j);
         bad |= at < 0;
@@ -96,18 +106,24 @@ __global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid
       }
       if (bad) {
         at = -1;
-        if (lane == 0) raise_error(a.c.error, kErrIndex);
+        raise_error(a.c.error, kErrIndex);
       }
       pos = a.positions ? __ldg(a.positions + t) : j;
     }
-    if (lane == 0) s_row[i] = at;
-    for (int p = lane; p < a.rope.rot / 2; p += 32) {
-      float c, sn;
-      rope_angle(a.rope.turn[p], pos, a.rope.amplitude, c, sn);
-      s_angle[angle_at<V>(units, i, p)] = make_float2(c, sn);
-    }
+    s_row[i] = at;
+    s_pos[i] = pos;
   }
   __syncthreads();
+  const int pairs = a.rope.rot / 2;
+  if (pairs > 0) {
+    for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+      const int t = divided(i, a.pair_mul, a.pair_shift), p = i - t * pairs;
+      float c, sn;
+      rope_angle(a.rope.turn[p], s_pos[t], a.rope.amplitude, c, sn);
+      s_angle[angle_at<V>(units, t, p)] = make_float2(c, sn);
+    }
+    __syncthreads();
+  }
   const long long v_off = (long long)a.c.page_size * a.c.H * a.c.D;
   for (int r0 = slot; r0 < rows; r0 += kAhead * slots) {
 #pragma unroll
@@ -133,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_tokens_kernel(const __grid
 template <typename T, int V, bool kInter>
 static cudaError_t launch(const AppendTokensArgs& a, cudaStream_t stream) {
   const int units = a.c.D / (2 * V);
-  const int per_block = rope_tokens_per_block(a.n_tokens, a.c.H, units, kThreads, kMaxTokens);
+  int per_block = (a.n_tokens + 148 * kCtasPerSm - 1) / (148 * kCtasPerSm);   // all blocks at once
+  if (per_block > kMaxTokens) per_block = kMaxTokens;
   const int blocks = (a.n_tokens + per_block - 1) / per_block;
   return launch_pdl(append_tokens_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads),
                     (size_t)per_block * units * V * sizeof(float2), stream, a, units, per_block);

@@ -259,6 +259,7 @@ int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int
     a.positions = positions;
     a.n_tokens = n_tokens;
     pkv::page_divisor(c->num_heads, &a.head_mul, &a.head_shift);
+    pkv::page_divisor(a.rope.rot > 0 ? a.rope.rot / 2 : 1, &a.pair_mul, &a.pair_shift);
     const cudaError_t e = pkv::launch_append_tokens(a, c->dtype, (cudaStream_t)stream);
     return e == cudaSuccess ? (int)KV_OK : api_cuda_fail(e, "kv_append_tokens: launch");
   });

@@ -51,8 +51,8 @@ struct AppendTokensArgs {
   const int32_t* cu_new;      // [n_seqs + 1], or NULL: token s is sequence s's
   const int32_t* positions;   // [n_tokens], or NULL: the token's index in its sequence
   int n_tokens;
-  uint32_t head_mul;          // c.H as a divisor
-  int head_shift;
+  uint32_t head_mul, pair_mul;     // c.H and rope.rot / 2 as divisors
+  int head_shift, pair_shift;
   RopeTable rope;             // rot 0: none
 };
 

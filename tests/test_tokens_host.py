@@ -234,19 +234,14 @@ def test_page_divisor(tmp_path):
 
 
 def find_seq(cu, n, t):
-    """The kernel's search: 32 probes a round."""
-    lo, hi, reads = 0, n, []
+    """The kernel's search."""
+    lo, hi = 0, n
     while lo < hi:
-        step = (hi - lo + 31) // 32
-        k = 0
-        for lane in range(32):
-            probe = lo + (lane + 1) * step - 1
-            if probe < hi:
-                reads.append(probe + 1)
-                k += cu[probe + 1] <= t
-        lo = min(lo + k * step, hi)
-        hi = min(lo + step - 1, hi)
-    assert all(0 < i <= n for i in reads)
+        mid = (lo + hi) // 2
+        if cu[mid + 1] <= t:
+            lo = mid + 1
+        else:
+            hi = mid
     return lo
 
 
