@@ -7,29 +7,33 @@
 // Bound by the bytes of K and V: each is read once for the whole group of
 // query heads that shares it.
 //
-// Split. A unit is one (sequence, K/V head, group of at most `rows` query
-// heads); its tokens are cut into tiles. Every CTA works its own part of the
-// split out from the lengths, which are read on the device, so a captured
-// launch serves growing sequences:
-//   - while cutting every unit into parts of at most kPartTiles tiles gives no
-//     more parts than CTAs, each part is a CTA's: short units stay whole, and
-//     nothing is joined that would not pay for it;
-//   - else all units' tiles (and kUnitCost more each, for what a unit costs by
-//     itself) stand in one line, and CTA c of G takes the c-th G-th of it,
-//     whatever the sequences' lengths: no CTA waits for a long sequence.
-// A unit that lies in one CTA is written to `out` by it; of the others every
-// CTA leaves (max, sum, unnormalised O) in the workspace, and the CTA that
-// arrives last joins them, in their order along the sequence whichever CTA
+// Split. A head unit is a K/V head with a group of at most `rows` of its query
+// heads. A CTA has one head unit, and the CTAs with the same place in their
+// units' rows ("a rank") take the same tokens: the heads of a token lie side
+// by side in the pool, and read at the same time they cost the memory far
+// less than one after the other (16 heads of 64, 1.28 GB: 192 us against 222
+// with each head's tokens cut elsewhere). The sequences are cut into tiles.
+// Every CTA works its own part of the split out from the lengths, which are
+// read on the device, so a captured launch serves growing sequences:
+//   - while cutting every sequence into parts of at most kPartTiles tiles
+//     gives no more parts than ranks, each part is a rank's: short sequences
+//     stay whole, and nothing is joined that would not pay for it;
+//   - else all sequences' tiles (and kSeqCost more each, for what a sequence
+//     costs by itself) stand in one line, and rank r of R takes the r-th R-th
+//     of it, whatever the sequences' lengths: none waits for a long one.
+// A sequence that lies in one rank is written to `out` by it; of the others
+// every rank leaves (max, sum, unnormalised O) in the workspace, and the one
+// that arrives last joins them, in their order along the sequence whichever
 // that is: results do not depend on timing, and no CTA waits for another.
 // More than kJoin parts are joined in two rounds, kGroup neighbours first.
 //
 // In a CTA each warp takes every kWarps-th step of kStep tokens and keeps a
 // running max, sum and O of its own; no warp waits for another until the end
-// of the unit. Token rows are gathered by 16-byte asynchronous copies into a
+// of the sequence. Token rows are gathered by 16-byte asynchronous copies into a
 // ring per warp (rows past the end are zero-filled and masked, so what the
-// pool holds there is never read). The ring runs on into the CTA's next unit
-// while the warps of this one are joined, and the next unit's queries (and
-// new key and value) are in registers by then.
+// pool holds there is never read). The ring runs on into the CTA's next
+// sequence while the warps of this one are joined, and the next one's queries
+// (and new key and value) are in registers by then.
 //
 // The products run transposed on mma.sync m16n8k16, the query heads on the
 // N = 8 side: S^T = K Q^T (tokens x heads) and O^T += V^T P^T. K and V then
@@ -54,7 +58,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 8.f;   // growth of a score, in powers of two, that the running max lets pass
 constexpr int kPartTiles = 3;   // tiles (32 KB of K and V each) that are not worth a join
-constexpr int kUnitCost = 3;    // a unit's own cost in tiles
+constexpr int kSeqCost = 3;     // a sequence's own cost in tiles
 constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
 constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
@@ -85,8 +89,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The first token that the query of a sequence of `len` sees, and the tiles
-// of each of its units.
+// The first token that the query of a sequence of `len` sees, and its tiles.
 __device__ __forceinline__ int first_seen(const DecodeArgs& a, int len) {
   return a.window > 0 && len > a.window ? len - a.window : 0;
 }
@@ -130,30 +133,29 @@ __device__ __forceinline__ bool rope_pair(const RopeTable& t, int p, int& e0, in
   return on;
 }
 
-// How the tiles are split over the CTAs (above), and what is left of this
-// CTA's part. The host chooses tiles coarse enough for 31 bits.
+// How the tiles are split over the ranks (above), and what is left of this
+// one's part. The host chooses tiles coarse enough for 31 bits.
 struct Split {
-  bool by_parts;      // a part a CTA; else the line
-  uint32_t each, more;   // the line: CTAs below `more` take each + 1 places, the others `each`
-  uint32_t t, end;    // places [t, end) of the line (or parts of all units) are left
-  // Where place t lies: sequence, unit, place `at` of the unit's `size`.
+  bool by_parts;      // a part a rank; else the line
+  uint32_t each, more;   // the line: ranks below `more` take each + 1 places, the others `each`
+  uint32_t t, end;    // places [t, end) of the line (or parts of all sequences) are left
+  // Where place t lies: place `at` of the sequence's `size`.
   int seq;
-  uint32_t unit, at, size, tiles;
+  uint32_t at, size, tiles;
   int len, later;     // the lengths of seq and seq + 1: read a sequence ahead, as a load takes
                       // about a microsecond while the memory is busy
 
-  __device__ __forceinline__ uint32_t cta_of(uint32_t place) const {
+  __device__ __forceinline__ uint32_t rank_of(uint32_t place) const {
     const uint32_t lower = more * (each + 1);
     return place < lower ? place / (each + 1) : more + (place - lower) / each;
   }
 };
 
-// The tokens of one unit that the CTA takes.
+// The tokens of one sequence that the CTA takes.
 struct Piece {
   int seq, len;       // and the sequence's length
-  int unit;           // the unit in its sequence
   int tok0, tok1;     // tokens [tok0, tok1)
-  int c0, parts;      // the unit's first CTA, and in how many it lies
+  int r0, parts;      // the sequence's first rank, and in how many it lies
 };
 
 __device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
@@ -161,50 +163,40 @@ __device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
 }
 __device__ __forceinline__ uint32_t parts_of(uint32_t tiles) { return (tiles + kPartTiles - 1) / kPartTiles; }
 
-// The places of a unit of the split's current sequence.
-__device__ __forceinline__ void measure(const DecodeArgs& a, Split& l) {
-  l.tiles = tiles_of(a, l.len);
-  l.size = l.by_parts ? parts_of(l.tiles) : l.tiles ? l.tiles + kUnitCost : 0;
-}
+// On to the next sequence's places.
 __device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
   ++l.seq;
   l.len = held(a.c, l.later);
   l.later = raw_len(a, l.seq + 1);
-  measure(a, l);
+  l.tiles = tiles_of(a, l.len);
+  l.size = l.by_parts ? parts_of(l.tiles) : l.tiles ? l.tiles + kSeqCost : 0;
+  l.at = 0;
 }
 
-__device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t units, Split& l, Piece& p) {
+__device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t rank, Split& l, Piece& p) {
   while (l.t < l.end) {
-    if (l.at >= l.size) {   // on to the next unit
-      l.at = 0;
-      if (++l.unit >= units || l.size == 0) {
-        l.unit = 0;
-        do next_sequence(a, l);
-        while (l.size == 0 && l.seq < a.c.n_seqs);
-      }
-    }
+    while (l.at >= l.size && l.seq < a.c.n_seqs) next_sequence(a, l);
     if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
     uint32_t tile0, tile1;
     if (l.by_parts) {
       tile0 = (uint32_t)((unsigned long long)l.tiles * l.at / l.size);
       tile1 = (uint32_t)((unsigned long long)l.tiles * (l.at + 1) / l.size);
-      p.c0 = l.t - l.at;
+      p.r0 = l.t - l.at;
       p.parts = l.size;
       ++l.t;
       ++l.at;
     } else {
       const uint32_t n = min(l.end - l.t, l.size - l.at);
-      const uint32_t first = l.t - l.at;   // the unit's first place; its tiles begin kUnitCost later
-      tile0 = l.at > kUnitCost ? l.at - kUnitCost : 0;
-      tile1 = l.at + n > kUnitCost ? l.at + n - kUnitCost : 0;
-      p.c0 = tile0 == 0 ? blockIdx.x : l.cta_of(first + kUnitCost);
-      p.parts = (tile1 == l.tiles ? blockIdx.x : l.cta_of(first + l.size - 1)) - p.c0 + 1;
+      const uint32_t first = l.t - l.at;   // the sequence's first place; its tiles begin kSeqCost later
+      tile0 = l.at > kSeqCost ? l.at - kSeqCost : 0;
+      tile1 = l.at + n > kSeqCost ? l.at + n - kSeqCost : 0;
+      p.r0 = tile0 == 0 ? rank : l.rank_of(first + kSeqCost);
+      p.parts = (tile1 == l.tiles ? rank : l.rank_of(first + l.size - 1)) - p.r0 + 1;
       l.t += n;
       l.at += n;
     }
     if (tile0 == tile1) continue;
     p.seq = l.seq;
-    p.unit = l.unit;
     p.len = l.len;
     const int seen = first_seen(a, l.len);
     p.tok0 = seen + (int)(tile0 << a.tile_shift);
@@ -214,18 +206,17 @@ __device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t units, 
   return false;
 }
 
-// This CTA's part of the split. Each warp works it out by itself, a lane for
-// a stretch of the sequences.
-__device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t units) {
+// The rank's part of the split. Each warp works it out by itself, a lane for a
+// stretch of the sequences.
+__device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t rank) {
   const int lane = threadIdx.x % 32;
   const int stretch = (a.c.n_seqs + 31) / 32;
   const int s0 = min(lane * stretch, a.c.n_seqs), s1 = min(s0 + stretch, a.c.n_seqs);
-  unsigned long long mine = 0;   // places of the line below, parts above
+  unsigned long long mine = 0;   // places of the line below, parts above; both stay below 2^31
   for (int s = s0; s < s1; ++s) {
     const uint32_t tiles = tiles_of(a, seq_len(a.c, s));
-    mine += (unsigned long long)parts_of(tiles) << 32 | (tiles ? tiles + kUnitCost : 0);
+    mine += (unsigned long long)parts_of(tiles) << 32 | (tiles ? tiles + kSeqCost : 0);
   }
-  mine *= units;                 // both stay below 2^31
   unsigned long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -233,45 +224,40 @@ __device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t units) {
     if (lane >= d) upto += o;
   }
   const unsigned long long total = __shfl_sync(0xffffffffu, upto, 31);
+  const uint32_t parts = (uint32_t)(total >> 32), places = (uint32_t)total;
   Split l;
-  l.by_parts = (total >> 32) <= (uint32_t)a.grid;
-  const uint32_t c = blockIdx.x;
+  l.by_parts = parts <= (uint32_t)a.ranks;
   if (l.by_parts) {
-    l.t = min(c, (uint32_t)(total >> 32));
-    l.end = min(c + 1, (uint32_t)(total >> 32));
+    l.t = min(rank, parts);
+    l.end = min(rank + 1, parts);
     l.each = l.more = 0;
-  } else {
-    const uint32_t n = (uint32_t)total, g = a.grid;   // more places than CTAs
-    l.each = n / g;
-    l.more = n - l.each * g;
-    l.t = c * l.each + min(c, l.more);
-    l.end = l.t + l.each + (c < l.more ? 1 : 0);
+  } else {   // more places than ranks
+    l.each = places / a.ranks;
+    l.more = places - l.each * a.ranks;
+    l.t = rank * l.each + min(rank, l.more);
+    l.end = l.t + l.each + (rank < l.more ? 1 : 0);
   }
   const uint32_t last = l.by_parts ? (uint32_t)(upto >> 32) : (uint32_t)upto;
   const uint32_t size = l.by_parts ? (uint32_t)(mine >> 32) : (uint32_t)mine;
   const uint32_t here = __ballot_sync(0xffffffffu, l.t < last && l.t >= last - size);
   const int owner = here ? __ffs(here) - 1 : 31;
-  l.seq = __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner);
+  l.seq = __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner) - 1;
   uint32_t base = __shfl_sync(0xffffffffu, last - size, owner);   // the stretch's first place
-  l.unit = l.at = 0;
-  l.later = raw_len(a, l.seq);
-  --l.seq;
+  l.later = raw_len(a, l.seq + 1);
   for (;;) {   // to the sequence of place t within the stretch
     next_sequence(a, l);
-    if (l.seq >= a.c.n_seqs || l.t - base < l.size * units) break;
-    base += l.size * units;
+    if (l.seq >= a.c.n_seqs || l.t - base < l.size) break;
+    base += l.size;
   }
-  if (l.size) {
-    l.unit = (l.t - base) / l.size;
-    l.at = l.t - base - l.unit * l.size;
-  }
+  l.at = l.t - base;
   return l;
 }
 
-
-// A part of a unit: CTA c0 + p's, in that CTA's second slot if it opened the
-// unit, else in its first.
-__device__ __forceinline__ long long part_slot(int c0, int p) { return 2LL * (c0 + p) + (p == 0 ? 1 : 0); }
+// Part p of a sequence that rank r0 begins: the slot of the workspace of that
+// CTA, its second if it begins the sequence, else its first.
+__device__ __forceinline__ long long part_slot(const DecodeArgs& a, int r0, int p, uint32_t unit) {
+  return 2LL * ((long long)(r0 + p) * a.units + unit) + (p == 0 ? 1 : 0);
+}
 
 // Adds one to a counter; true for the arrival that completes `of`, with the
 // others' writes visible to it. Called by one thread, after a barrier behind
@@ -284,28 +270,29 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
   return last;
 }
 
-// Joins parts p0, p0 + step, ... (n of at most 32) of the unit begun by CTA
-// c0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
-// writes O / l to `out` (the unit's first query row), others the part in the
+// Joins parts p0, p0 + step, ... (n of at most 32) of the sequence begun by
+// rank r0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
+// writes O / l to `out` (the unit's first query row of the sequence), others the part in the
 // first one's place. A warp takes a query head at a time, a lane a part's
 // weight, then all lanes the parts' rows with kPre of them in flight, the
 // first before the weights are known.
 template <int D, typename T, int kRows>
-__device__ __forceinline__ void join_parts(const DecodeArgs& a, int c0, int p0, int step, int n, int heads, T* out) {
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, int r0, uint32_t unit, int p0, int step, int n, int heads,
+                                           T* out) {
   constexpr int V = D / 32;    // values of a lane
   constexpr int kPre = 8; 
   using P = Pack<float, V>;
   const int lane = threadIdx.x % 32;
+  auto slot = [&](int k) { return part_slot(a, r0, p0 + k * step, unit) * kRows; };
   for (int i = threadIdx.x / 32; i < heads; i += kWarps) {
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + i;
     P* rows = reinterpret_cast<P*>(a.part_o) + i * 32 + lane;
-    const long long mine = part_slot(c0, p0 + min(lane, n - 1) * step) * kRows;
-    const float2 x = __ldcg(ml + mine);
+    const float2 x = __ldcg(ml + slot(min(lane, n - 1)));
     float acc[V] = {};
     P y[kPre];
 #pragma unroll
     for (int k = 0; k < kPre; ++k)
-      if (k < n) y[k] = load_cg(rows + part_slot(c0, p0 + k * step) * kRows * 32);
+      if (k < n) y[k] = load_cg(rows + slot(k) * 32);
     const float m = lane < n ? x.x : -INFINITY;
     float top = m;
 #pragma unroll
@@ -324,7 +311,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, int c0, int p0, 
       }
 #pragma unroll
       for (int k = 0; k < kPre; ++k)
-        if (k0 + kPre + k < n) y[k] = load_cg(rows + part_slot(c0, p0 + (k0 + kPre + k) * step) * kRows * 32);
+        if (k0 + kPre + k < n) y[k] = load_cg(rows + slot(k0 + kPre + k) * 32);
     }
     if (out) {
       const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
@@ -335,7 +322,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, int c0, int p0, 
       P r;
 #pragma unroll
       for (int e = 0; e < V; e += 2) r.set2(e / 2, acc[e], acc[e + 1]);
-      const long long at = part_slot(c0, p0) * kRows;
+      const long long at = slot(0);
       rows[at * 32] = r;
       if (lane == 0) reinterpret_cast<float2*>(a.part_ml)[at + i] = make_float2(top, sum);
     }
@@ -353,12 +340,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const uint32_t units = a.c.H * a.head_groups;   // of a sequence
+  const uint32_t rank = blockIdx.x / a.units, unit = blockIdx.x - rank * a.units;
+  const int h = unit / a.head_groups;                                   // its K/V head
+  const int head0 = (unit - h * a.head_groups) * kRows;                 // and query heads, within the head's group
+  const int heads = a.group - head0 < kRows ? a.group - head0 : kRows;
+  const int q0 = h * a.group + head0;
 
   pdl_wait();      // the pool, the tables and the queries may come from earlier kernels
   pdl_trigger();
 
-  Split work = split(a, units);
+  Split work = split(a, rank);
   T* out = static_cast<T*>(a.out);
   const int q_heads = a.c.H * a.group;
   for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x) {
@@ -380,19 +371,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   constexpr int kPerPass = 32 / S::kChunks;   // rows of a pass
   const int chunk = lane % S::kChunks;
   const long long row_size = (long long)a.c.H * D;
+  const T* const src0 = pool + h * D + chunk * 8;                 // the lane's chunk of the head in row 0
   int l_seq = 0, l_len = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
-  const T* l_src = nullptr;                                       // the lane's chunk of the unit's head in row 0
   int l_row = -1;                                                 // the lane's row of the next step, looked up ahead
   bool l_ok = false;
   auto look_up = [&]() {   // goes on to the next piece where this one has no step left
     while (l_next >= l_end) {
       Piece p;
-      if (!next_piece(a, units, ahead, p)) {
+      if (!next_piece(a, rank, ahead, p)) {
         l_next = INT_MAX;
         return;
       }
       l_seq = p.seq;
-      l_src = pool + p.unit / a.head_groups * D + chunk * 8;
       l_len = p.len;
       l_end = p.tok1;
       l_next = p.tok0 + warp * S::kStep;   // a piece may have no step for this warp
@@ -413,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     for (int r0 = 0; r0 < S::kStep; r0 += kPerPass) {
       const int r = r0 + lane / S::kChunks;
       const int from = __shfl_sync(0xffffffffu, l_row, r);
-      const T* src = l_src + max(from, 0) * row_size;
+      const T* src = src0 + max(from, 0) * row_size;
       const uint32_t dst = dst0 + r * (D * 2) + ((chunk ^ (r & 7)) << 4);
       cp_async16(dst, src, from >= 0);
       cp_async16(dst + S::kHalf, src + v_off, from >= 0);
@@ -437,12 +427,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   uint4 raw[kQ], raw_new = make_uint4(0, 0, 0, 0);
   int new_page = -1, new_pos = -1;
   auto request = [&](const Piece& p) {
-    const int h = p.unit / a.head_groups, head0 = p.unit % a.head_groups * kRows;
-    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + (h * a.group + head0) * a.q.head_stride;
+    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + q0 * a.q.head_stride;
 #pragma unroll
     for (int x = 0; x < kQ; ++x) {
       const int i = (x * kThreads + tid) / S::kChunks, chunk = tid % S::kChunks;
-      raw[x] = i < kRows && head0 + i < a.group ? *reinterpret_cast<const uint4*>(q + i * a.q.head_stride + chunk * 8)
+      raw[x] = i < heads ? *reinterpret_cast<const uint4*>(q + i * a.q.head_stride + chunk * 8)
                                                 : make_uint4(0, 0, 0, 0);
     }
     if (kFused) {
@@ -465,13 +454,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
   int stage = 0;
   Piece p;
-  bool more = next_piece(a, units, work, p);
+  bool more = next_piece(a, rank, work, p);
   if (more) request(p);
   while (more) {
-    const int h = p.unit / a.head_groups;
-    const int head0 = p.unit % a.head_groups * kRows;                     // within the K/V head's group
-    const int heads = a.group - head0 < kRows ? a.group - head0 : kRows;
-    const int q0 = h * a.group + head0;
     const int tok0 = p.tok0 + warp * S::kStep, tok1 = p.tok1;
     const bool has_new = kFused && tok1 == p.len;   // the new token's row lies in this piece
     Piece next;
@@ -486,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     const int row_of_new = row_in(a.c, new_page, p.len - 1);
     const int pos = a.positions ? new_pos : p.len - 1;
     if (has_new && tid < 2 * S::kChunks) reinterpret_cast<uint4*>(sn)[tid] = raw_new;
-    more = next_piece(a, units, work, next);
+    more = next_piece(a, rank, work, next);
     if (more) request(next);
     if (kFused) {
       float c = 1.f, s = 0.f;
@@ -674,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     float* wo = reinterpret_cast<float*>(smem + M::kOffO);
     float* wml = reinterpret_cast<float*>(smem + M::kOffMl);
     const bool whole = p.parts == 1;
-    const long long slot = part_slot(p.c0, blockIdx.x - p.c0);
+    const long long slot = part_slot(a, p.r0, rank - p.r0, unit);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n > 0 && heads <= n * 8) break;
@@ -721,27 +706,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       }
     }
     if (!whole) {
-      // The parts of the unit, this CTA's among them; the last to arrive joins.
+      // The sequence's parts, this CTA's among them; the last to arrive joins.
       T* to = out + ((long long)p.seq * q_heads + q0) * D;
       const bool two = p.parts > kJoin;
-      const int me = blockIdx.x - p.c0, g0 = two ? me / kGroup * kGroup : 0;
+      const int me = rank - p.r0, g0 = two ? me / kGroup * kGroup : 0;
       const int of = two ? min(kGroup, p.parts - g0) : p.parts;
       const int groups = (p.parts + kGroup - 1) / kGroup;
       __syncthreads();
       if (tid == 0) {
         const bool ready = *a.ws_magic == kWorkspaceMagic;
         if (!ready) raise_error(a.c.error, kErrWorkspace);
-        s_last = ready && arrive_last(a.counters + part_slot(p.c0, g0), of);
+        s_last = ready && arrive_last(a.counters + part_slot(a, p.r0, g0, unit), of);
       }
       __syncthreads();
       bool last = s_last;
-      if (last) join_parts<D, T, kRows>(a, p.c0, g0, 1, of, heads, two ? nullptr : to);
+      if (last) join_parts<D, T, kRows>(a, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
       if (last && two) {
         __syncthreads();
-        if (tid == 0) s_last = arrive_last(a.counters + 2 * a.grid + part_slot(p.c0, 0), groups);
+        if (tid == 0) s_last = arrive_last(a.counters + 2 * gridDim.x + part_slot(a, p.r0, 0, unit), groups);
         __syncthreads();
         last = s_last;
-        if (last) join_parts<D, T, kRows>(a, p.c0, 0, kGroup, groups, heads, to);
+        if (last) join_parts<D, T, kRows>(a, p.r0, unit, 0, kGroup, groups, heads, to);
       }
     }
     p = next;
@@ -751,14 +736,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
 int decode_rows(int group) { return group <= 8 ? 8 : 16; }
 
-int decode_grid(int num_sms) { return num_sms * kCtasPerSm; }
+// One, with a CTA a unit, where the units alone fill the GPU.
+int decode_ranks(int units, int num_sms) {
+  const int n = num_sms * kCtasPerSm / units;
+  return n > 1 ? n : 1;
+}
 
 // log2 of the tokens of a tile: the finest that keeps the line of the longest
-// possible sequences, every unit's cost included, within 31 bits.
-int decode_tile_shift(int D, int n_seqs, int units, long long most_tokens) {
+// possible sequences, every sequence's cost included, within 31 bits.
+int decode_tile_shift(int D, int n_seqs, long long most_tokens) {
   int shift = D == 64 ? 7 : 6;
   static_assert(Shape<64>::kStride == 128 && Shape<128>::kStride == 64, "the finest tile is a step of all warps");
-  while (((most_tokens >> shift) + 1 + kUnitCost) * n_seqs * units > INT_MAX && shift < 30) ++shift;
+  while (((most_tokens >> shift) + 1 + kSeqCost) * n_seqs > INT_MAX) ++shift;
   return shift;
 }
 
@@ -768,7 +757,7 @@ static cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   constexpr int kBytes = Smem<D, NT>::kBytes;
   const cudaError_t e = ensure_dynamic_smem(decode_kernel<D, T, NT, kFused>, kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<D, T, NT, kFused>, dim3(a.grid), dim3(kThreads), kBytes, stream, a);
+  return launch_pdl(decode_kernel<D, T, NT, kFused>, dim3(a.ranks * a.units), dim3(kThreads), kBytes, stream, a);
 }
 
 template <int D, typename T>

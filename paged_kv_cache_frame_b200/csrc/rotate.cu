@@ -13,17 +13,17 @@
 namespace pkv {
 
 namespace {
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;    // of a block; twice as many for heads of more units (KV_MAX_ROTATE_DIM in single values)
 constexpr int kAhead = 2;        // rows in flight per thread
 constexpr int kMaxTokens = 16;   // tokens of a block
 }  // namespace
 
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_constant__ RotateArgs a, int units,
+__global__ void __launch_bounds__(2 * kThreads, 4) rotate_kernel(const __grid_constant__ RotateArgs a, int units,
                                                           int per_block) {
   extern __shared__ __align__(16) float2 s_angle[];
   const int u = threadIdx.x % units;
-  const int slot = threadIdx.x / units, slots = kThreads / units;
+  const int slot = threadIdx.x / units, slots = blockDim.x / units;   // at least one
   const int first = (int)blockIdx.x * per_block;
   const int tokens = min(per_block, a.n_tokens - first);
   const int rows = tokens * a.n_heads;
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
   };
   load(slot);   // on their way while the angles are worked out
   const int pairs = a.rope.rot / 2;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
     const int t = i / pairs, p = i - t * pairs;
     float c, s;
     rope_angle(a.rope.turn[p], __ldg(a.positions + first + t), a.rope.amplitude, c, s);
@@ -73,9 +73,11 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_consta
 template <typename T, int V, bool kInter>
 static cudaError_t launch(const RotateArgs& a, cudaStream_t stream) {
   const int units = (a.head_dim + 2 * V - 1) / (2 * V);
-  const int per_block = rope_tokens_per_block(a.n_tokens, a.n_heads, units, kThreads, kMaxTokens);
+  static_assert(KV_MAX_ROTATE_DIM / 2 <= 2 * kThreads, "a thread a unit");
+  const int threads = units > kThreads ? 2 * kThreads : kThreads;
+  const int per_block = rope_tokens_per_block(a.n_tokens, a.n_heads, units, threads, kMaxTokens);
   const int blocks = (a.n_tokens + per_block - 1) / per_block;
-  return launch_pdl(rotate_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads),
+  return launch_pdl(rotate_kernel<T, V, kInter>, dim3(blocks), dim3(threads),
                     (size_t)per_block * units * V * sizeof(float2), stream, a, units, per_block);
 }
 

@@ -89,25 +89,28 @@ int view_rope(const kv_rope_t* r, int head_dim, const std::string& who, pkv::Rop
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// [magic | arrival counters | the parts' maxima and sums | their outputs]
+// [magic | arrival counters | the parts' maxima and sums | their outputs];
+// nothing is split where a unit has one CTA.
 struct DecodeLayout {
-  int grid;
-  size_t off_counters, off_ml, off_o, total;
+  int units, ranks;
+  size_t counters, off_counters, off_ml, off_o, total;
 };
 
-DecodeLayout decode_layout(int D, int group) {
+DecodeLayout decode_layout(const kv_tokens* c, int q_heads) {
+  const int group = q_heads / c->num_heads, rows = pkv::decode_rows(group);
   DecodeLayout l;
-  l.grid = pkv::decode_grid(pkv::current_device_sms());
-  const size_t slots = 2 * (size_t)l.grid * pkv::decode_rows(group);
+  l.units = c->num_heads * ((group + rows - 1) / rows);
+  l.ranks = pkv::decode_ranks(l.units, pkv::current_device_sms());
+  const size_t ctas = l.ranks > 1 ? (size_t)l.ranks * l.units : 0;
+  l.counters = 4 * ctas * sizeof(uint32_t);
   l.off_counters = 256;
-  l.off_ml = align256(l.off_counters + (size_t)l.grid * 16);
-  l.off_o = align256(l.off_ml + slots * 8);
-  l.total = align256(l.off_o + slots * D * 4);
+  l.off_ml = align256(l.off_counters + l.counters);
+  l.off_o = align256(l.off_ml + 2 * ctas * rows * 8);
+  l.total = align256(l.off_o + 2 * ctas * rows * c->head_dim * 4);
   return l;
 }
 
 int check_group(const kv_tokens* c, int q_heads, const std::string& who) {
-  // With KV_MAX_TOKEN_SEQS the bound leaves the units' count below 2^27.
   if (q_heads < 1 || q_heads > KV_MAX_Q_HEADS || q_heads % c->num_heads != 0)
     return api_fail(KV_ERR_ARG, who + ": q_heads must be a multiple of the pool's heads, at most KV_MAX_Q_HEADS");
   return KV_OK;
@@ -132,7 +135,7 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   if (fused && (rc = view_rows(v, "v", who, &a.v)) != KV_OK) return rc;
   if (!out || !aligned(out, 16)) return api_fail(KV_ERR_ARG, who + ": out NULL or not 16-byte aligned");
   a.group = q_heads / c->num_heads;
-  const DecodeLayout l = decode_layout(c->head_dim, a.group);
+  const DecodeLayout l = decode_layout(c, q_heads);
   if (!workspace || !aligned(workspace, 16)) return api_fail(KV_ERR_ARG, who + ": workspace NULL or not 16-byte aligned");
   if (workspace_bytes < l.total) return api_fail(KV_ERR_CAPACITY, who + ": workspace smaller than kv_decode_workspace_bytes()");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -145,9 +148,9 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   const int rows = pkv::decode_rows(a.group);
   a.head_groups = (a.group + rows - 1) / rows;
   a.window = window;
-  a.grid = l.grid;
-  a.tile_shift = pkv::decode_tile_shift(c->head_dim, c->n_seqs, c->num_heads * a.head_groups,
-                                        (long long)c->table_width * c->page_size);
+  a.units = l.units;
+  a.ranks = l.ranks;
+  a.tile_shift = pkv::decode_tile_shift(c->head_dim, c->n_seqs, (long long)c->table_width * c->page_size);
   const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
   a.scale_log2 = (float)(s * 1.4426950408889634);
   const cudaError_t e = pkv::launch_decode(a, c->dtype, fused, (cudaStream_t)stream);
@@ -271,7 +274,7 @@ size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads) {
     pkv::TokenCache view;
     if (view_cache(c, "kv_decode_workspace_bytes", &view) != KV_OK) return 0;
     if (check_group(c, q_heads, "kv_decode_workspace_bytes") != KV_OK) return 0;
-    n = decode_layout(c->head_dim, q_heads / c->num_heads).total;
+    n = decode_layout(c, q_heads).total;
     return 0;
   });
   return n;
@@ -284,12 +287,12 @@ int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, s
     int rc = view_cache(c, who, &view);
     if (rc != KV_OK) return rc;
     if ((rc = check_group(c, q_heads, who)) != KV_OK) return rc;
-    const DecodeLayout l = decode_layout(c->head_dim, q_heads / c->num_heads);
+    const DecodeLayout l = decode_layout(c, q_heads);
     if (!workspace || !aligned(workspace, 16)) return api_fail(KV_ERR_ARG, who + ": workspace NULL or not 16-byte aligned");
     if (workspace_bytes < l.total) return api_fail(KV_ERR_CAPACITY, who + ": workspace smaller than kv_decode_workspace_bytes()");
     static_assert(pkv::kWorkspaceMagic == 0xa5a5a5a5u, "the magic is one byte over and over");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    cudaError_t e = cudaMemsetAsync(ws + l.off_counters, 0, (size_t)l.grid * 16, (cudaStream_t)stream);
+    cudaError_t e = cudaMemsetAsync(ws + l.off_counters, 0, l.counters, (cudaStream_t)stream);
     if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0xa5, 4, (cudaStream_t)stream);
     return e == cudaSuccess ? (int)KV_OK : api_cuda_fail(e, "kv_decode_workspace_init: memset");
   });

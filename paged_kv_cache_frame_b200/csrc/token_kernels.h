@@ -65,13 +65,13 @@ struct DecodeArgs {
   RowsIn k, v;                // the new tokens (fused append), else NULL
   const int32_t* positions;   // [n_seqs], or NULL: len - 1
   const uint32_t* ws_magic;   // kWorkspaceMagic where the workspace was prepared
-  uint32_t* counters;         // [4 * grid] arrivals, zero between launches
-  float* part_ml;             // [2 * grid][rows][2]
-  float* part_o;              // [2 * grid][rows][D]
+  uint32_t* counters;         // [4 * CTAs] arrivals, zero between launches
+  float* part_ml;             // [2 * CTAs][rows][2]
+  float* part_o;              // [2 * CTAs][rows][D]
   int group;                  // query heads a K/V head serves
   int head_groups;            // groups of at most `rows` query heads a unit takes
   int window;                 // 0: the whole cache
-  int grid;                   // CTAs of the attention launch
+  int units, ranks;           // CTAs: H * head_groups units, `ranks` of each
   int tile_shift;             // log2 of a tile's tokens
   float scale_log2;           // scale * log2(e)
   RopeTable rope;
@@ -79,10 +79,10 @@ struct DecodeArgs {
 
 cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_append_tokens(const AppendTokensArgs& a, int dtype, cudaStream_t stream);
-// Query heads one unit takes (8 or 16) and CTAs of a launch.
+// Query heads one unit takes (8 or 16), CTAs of a unit, log2 of a tile's tokens.
 int decode_rows(int group);
-int decode_grid(int num_sms);
-int decode_tile_shift(int D, int n_seqs, int units, long long most_tokens);
+int decode_ranks(int units, int num_sms);
+int decode_tile_shift(int D, int n_seqs, long long most_tokens);
 cudaError_t launch_decode(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
 
 }  // namespace pkv

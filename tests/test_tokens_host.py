@@ -262,83 +262,83 @@ def test_sequence_search():
 
 
 JOIN, GROUP = 32, 16      # parts joined in one round, and neighbours joined first where there are more
-PART, COST = 3, 3         # tiles a part holds at most, a unit's own cost in the line
+PART, COST = 3, 3         # tiles a part holds at most, a sequence's own cost in the line
 
 
-def split_pieces(tiles, units, grid):
-    """The pieces of every CTA as the attention kernel splits them: unit key,
-    CTA, tiles, the unit's first CTA and its parts."""
+def split_pieces(tiles, ranks):
+    """The pieces of every rank as the attention kernel splits them: sequence,
+    rank, tiles, the sequence's first rank and its parts."""
     parts_of = lambda n: (n + PART - 1) // PART  # noqa: E731
-    n_parts = sum(parts_of(n) * units for n in tiles)
-    by_parts = n_parts <= grid
-    total = sum((n + COST) * units for n in tiles if n)
-    each, more = divmod(total, grid)
+    n_parts = sum(parts_of(n) for n in tiles)
+    by_parts = n_parts <= ranks
+    each, more = divmod(sum(n + COST for n in tiles if n), ranks)
 
-    def cta_of(place):
+    def rank_of(place):
         lower = more * (each + 1)
         return place // (each + 1) if place < lower else more + (place - lower) // each
 
     pieces = []
-    for c in range(grid):
+    for r in range(ranks):
         if by_parts:
-            t, end = min(c, n_parts), min(c + 1, n_parts)
+            t, end = min(r, n_parts), min(r + 1, n_parts)
         else:
-            t = c * each + min(c, more)
-            end = t + each + (c < more)
+            t = r * each + min(r, more)
+            end = t + each + (r < more)
         base, seq = 0, 0
         while t < end:
             while True:
                 n = tiles[seq]
                 size = parts_of(n) if by_parts else n + COST if n else 0
-                if t - base < size * units:
+                if t - base < size:
                     break
-                base += size * units
+                base += size
                 seq += 1
-            unit, at = divmod(t - base, size)
+            at = t - base
             if by_parts:
                 t0, t1 = n * at // size, n * (at + 1) // size
-                c0, parts = t - at, size
+                r0, parts = t - at, size
                 t += 1
             else:
                 took = min(end - t, size - at)
                 t0, t1 = max(0, at - COST), max(0, at + took - COST)
                 first = t - at
-                c0 = cta_of(first + COST)
-                parts = cta_of(first + size - 1) - c0 + 1
+                r0 = r if t0 == 0 else rank_of(first + COST)
+                parts = (r if t1 == n else rank_of(first + size - 1)) - r0 + 1
                 t += took
             if t0 < t1:
-                pieces.append(((seq, unit), c, t0, t1, c0, parts))
+                pieces.append((seq, r, t0, t1, r0, parts))
     return pieces
 
 
 @pytest.mark.parametrize("seed", range(120))
 def test_split_covers_every_tile_and_the_join_finds_the_parts(seed):
-    """Every tile once; a unit's parts in neighbouring CTAs and slots no other
-    part has; arrivals counted to the number that comes, on counters no two
-    units share."""
+    """Every tile once; a sequence's parts in neighbouring ranks and slots no
+    other part has; arrivals counted to the number that comes, on counters no
+    two sequences (and no two units) share."""
     rng = random.Random(seed)
-    seqs, units, grid = rng.choice([1, 2, 7, 64, 300]), rng.choice([1, 2, 8, 24]), rng.choice([1, 4, 296])
+    seqs, ranks, units = rng.choice([1, 2, 7, 64, 300]), rng.choice([1, 4, 37, 296]), rng.choice([1, 3])
     most = rng.choice([3, 20, 400, 9000])
     tiles = [rng.choice([0, 1, 2, 5, rng.randint(0, most)]) for _ in range(seqs)]
-    pieces = split_pieces(tiles, units, grid)
-    assert set(k for k, *_ in pieces) == {(s, u) for s in range(seqs) if tiles[s] for u in range(units)}
-    by_unit, slots, first, second = {}, set(), {}, {}
-    for key, c, t0, t1, c0, n in pieces:
-        by_unit.setdefault(key, []).append((t0, t1, c, c0, n))
-        if n > 1:
-            slot = 2 * c + (c == c0)
-            assert slot < 2 * grid and slot not in slots
-            slots.add(slot)
-            two, me = n > JOIN, c - c0
+    pieces = split_pieces(tiles, ranks)
+    assert set(p[0] for p in pieces) == {s for s in range(seqs) if tiles[s]}
+    by_seq, slots, first, second = {}, set(), {}, {}
+    slot = lambda r0, p, u: 2 * ((r0 + p) * units + u) + (p == 0)  # noqa: E731
+    for seq, r, t0, t1, r0, n in pieces:
+        by_seq.setdefault(seq, []).append((t0, t1, r, r0, n))
+        assert n == 1 or ranks > 1
+        for u in range(units if n > 1 else 0):
+            here = slot(r0, r - r0, u)
+            assert here < 2 * ranks * units and here not in slots
+            slots.add(here)
+            two, me = n > JOIN, r - r0
             g0 = me // GROUP * GROUP if two else 0
-            counter = 2 * (c0 + g0) + (g0 == 0)
-            first.setdefault(counter, []).append((key, min(GROUP, n - g0) if two else n))
+            first.setdefault(slot(r0, g0, u), []).append((seq, u, min(GROUP, n - g0) if two else n))
             if two and me == g0:
-                second.setdefault(2 * c0 + 1, []).append((key, (n + GROUP - 1) // GROUP))
+                second.setdefault(slot(r0, 0, u), []).append((seq, u, (n + GROUP - 1) // GROUP))
     for counters in (first, second):
         for arrivals in counters.values():
-            assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][1] <= JOIN
-    for (seq, _), p in by_unit.items():
+            assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][2] <= JOIN
+    for seq, p in by_seq.items():
         p.sort()
         assert p[0][0] == 0 and p[-1][1] == tiles[seq] and all(a[1] == b[0] for a, b in zip(p, p[1:]))
         assert [x[2:] for x in p] == [(p[0][3] + i, p[0][3], len(p)) for i in range(len(p))]
