@@ -23,6 +23,7 @@ from . import capi
 from .capi import (KV_BF16, KV_FP16, KV_FP32, KV_ROPE_HALF, KV_ROPE_INTERLEAVED, KV_ROPE_LINEAR, KV_ROPE_NONE,
                    KV_ROPE_NTK, KV_ROPE_YARN)
 
+_kv_rows = capi.kv_rows
 LAYOUTS = {"half": KV_ROPE_HALF, "interleaved": KV_ROPE_INTERLEAVED}
 SCALINGS = {"none": KV_ROPE_NONE, "linear": KV_ROPE_LINEAR, "ntk": KV_ROPE_NTK, "yarn": KV_ROPE_YARN}
 
@@ -111,7 +112,7 @@ def _bind_torch():
 def _check(x, name, shape, dtype, device, contiguous=True):
     """Shape, dtype, layout and device of a tensor, before its address goes to
     the library. Not contiguous: the last dimension only has to be dense."""
-    if (x.shape == shape and x.dtype is dtype and x.device == device
+    if (x.dtype is dtype and x.shape == shape and x.device == device
             and (x.is_contiguous() or (not contiguous and x.stride(-1) == 1))):
         return
     if tuple(x.shape) != tuple(shape):
@@ -138,7 +139,7 @@ def _rows(x):
     one element says nothing and is 0."""
     n, h, _ = x.shape
     t, s, _ = x.stride()
-    return capi.kv_rows(x.data_ptr(), t if n > 1 else 0, s if h > 1 else 0)
+    return _kv_rows(x.data_ptr(), t if n > 1 else 0, s if h > 1 else 0)
 
 
 class _On:
@@ -174,9 +175,16 @@ class _On:
 def _here(device, stream):
     """The current stream's handle where a call needs no switch of device or
     stream, else None (_On makes it)."""
-    if stream is None and device.type == "cuda" and torch.cuda.current_device() == device.index:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None and device.type == "cuda":
+        i = device.index
+        if torch._C._cuda_getDevice() == i:
+            return torch._C._cuda_getCurrentRawStream(i)
     return None
+
+
+def _like(x):
+    """An uninitialised contiguous tensor of x's shape."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 @functools.lru_cache(maxsize=None)
@@ -188,7 +196,8 @@ def _rotation_with_gradient():
         @staticmethod
         def forward(ctx, x, positions, rope, inverse):
             ctx.save_for_backward(positions)
-            ctx.rope, ctx.inverse = rope, inverse
+            ctx.rope = rope
+            ctx.inverse = inverse
             return rope._rotate(x, positions, None, inverse, None)
 
         @staticmethod
@@ -230,6 +239,7 @@ class Rope:
         else:
             self.handle = kv_rope_init(rot_dim, LAYOUTS[layout], SCALINGS[scaling], base, factor, original_context,
                                        low_turns, high_turns, amplitude or 0.0)
+        self._lib = capi.lib()
         got = kv_rope_get(self.handle)
         self.rot_dim, self.layout, self.amplitude, self.inv_freq = rot_dim, layout, got["amplitude"], got["theta"]
 
@@ -262,8 +272,8 @@ class Rope:
     def _launch(self, x, positions, out, inverse, code, s):
         n, h, d = x.shape
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        rc = capi.lib().kv_rotate(self.handle, _rows(x), _rows(out), positions.data_ptr(), n, h, d, code, inverse, s)
+            out = _like(x)
+        rc = self._lib.kv_rotate(self.handle, _rows(x), _rows(out), positions.data_ptr(), n, h, d, code, inverse, s)
         if rc:
             capi.check(rc, "kv_rotate")
         return out
@@ -311,6 +321,7 @@ class PagedTokens:
             pool.data_ptr(), tables.data_ptr(), lens.data_ptr(), self.error.data_ptr(),
             tables.stride(0) if self.n_seqs > 1 else width, self.max_pages, self.page_size, self.H, self.D,
             _codes[pool.dtype], width, self.n_seqs)
+        self._lib = capi.lib()
         self._bytes = {}        # query heads -> workspace bytes
         self._workspaces = {}   # (stream, query heads) -> the workspace of eager calls there
 
@@ -373,7 +384,7 @@ class PagedTokens:
             return self._append(k, v, n, cu, rope, pos, s)
 
     def _append(self, k, v, n, cu, rope, pos, s):
-        rc = capi.lib().kv_append_tokens(self._c, _rows(k), _rows(v), n, cu, rope.handle if rope is not None else None,
+        rc = self._lib.kv_append_tokens(self._c, _rows(k), _rows(v), n, cu, rope.handle if rope is not None else None,
                                          pos, s)
         if rc:
             capi.check(rc, "kv_append_tokens")
@@ -414,10 +425,10 @@ class PagedTokens:
 
     def _buffers(self, q, out, workspace, s):
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _like(q)
         if workspace is None:
             heads = q.shape[1]
-            if torch.cuda.is_current_stream_capturing():
+            if torch._C._cuda_isCurrentStreamCapturing():
                 workspace = self._new_workspace(heads, s)   # the graph's own, prepared by each replay
             else:
                 workspace = self._workspaces.get((s, heads))
@@ -441,8 +452,8 @@ class PagedTokens:
 
     def _decode(self, q, out, scale, window, workspace, s):
         out, ws = self._buffers(q, out, workspace, s)
-        rc = capi.lib().kv_decode(self._c, _rows(q), q.shape[1], scale or 0.0, window, out.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), s)
+        rc = self._lib.kv_decode(self._c, _rows(q), q.shape[1], scale or 0.0, window, out.data_ptr(), ws.data_ptr(),
+                                  ws.nbytes, s)
         if rc:
             capi.check(rc, "kv_decode")
         return out
@@ -466,9 +477,9 @@ class PagedTokens:
 
     def _decode_append(self, k, v, q, rope, pos, out, scale, window, workspace, s):
         out, ws = self._buffers(q, out, workspace, s)
-        rc = capi.lib().kv_decode_append(self._c, _rows(k), _rows(v), _rows(q), q.shape[1],
+        rc = self._lib.kv_decode_append(self._c, _rows(k), _rows(v), _rows(q), q.shape[1],
                                          rope.handle if rope is not None else None, pos, scale or 0.0, window,
-                                         out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+                                         out.data_ptr(), ws.data_ptr(), ws.nbytes, s)
         if rc:
             capi.check(rc, "kv_decode_append")
         return out
