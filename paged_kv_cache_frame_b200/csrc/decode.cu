@@ -179,8 +179,8 @@ __device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t rank, S
     if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
     uint32_t tile0, tile1;
     if (l.by_parts) {
-      tile0 = (uint32_t)((unsigned long long)l.tiles * l.at / l.size);
-      tile1 = (uint32_t)((unsigned long long)l.tiles * (l.at + 1) / l.size);
+      tile0 = l.tiles * l.at / l.size;   // tiles <= kPartTiles * ranks here
+      tile1 = l.tiles * (l.at + 1) / l.size;
       p.r0 = l.t - l.at;
       p.parts = l.size;
       ++l.t;
@@ -273,18 +273,21 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
 // Joins parts p0, p0 + step, ... (n of at most 32) of the sequence begun by
 // rank r0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
 // writes O / l to `out` (the unit's first query row of the sequence), others the part in the
-// first one's place. A warp takes a query head at a time, a lane a part's
-// weight, then all lanes the parts' rows with kPre of them in flight, the
-// first before the weights are known.
+// first one's place. A warp takes a query head at a time (of one or two
+// heads all warps, each some of the parts, added up in `sums`), a lane a
+// part's weight, then all lanes the parts' rows with kPre of them in flight,
+// the first before the weights are known. All threads of the CTA.
 template <int D, typename T, int kRows>
-__device__ __forceinline__ void join_parts(const DecodeArgs& a, int r0, uint32_t unit, int p0, int step, int n, int heads,
-                                           T* out) {
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, float* sums, int r0, uint32_t unit, int p0, int step, int n,
+                                           int heads, T* out) {
   constexpr int V = D / 32;    // values of a lane
-  constexpr int kPre = 8; 
+  constexpr int kPre = 8;
   using P = Pack<float, V>;
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int share = heads == 1 ? kWarps : heads == 2 ? kWarps / 2 : 1;   // warps of a head
+  const int k1 = warp % share;                                           // this warp's parts: k1, k1 + share, ...
   auto slot = [&](int k) { return part_slot(a, r0, p0 + k * step, unit) * kRows; };
-  for (int i = threadIdx.x / 32; i < heads; i += kWarps) {
+  for (int i = warp / share; i < heads; i += kWarps / share) {
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + i;
     P* rows = reinterpret_cast<P*>(a.part_o) + i * 32 + lane;
     const float2 x = __ldcg(ml + slot(min(lane, n - 1)));
@@ -292,7 +295,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, int r0, uint32_t
     P y[kPre];
 #pragma unroll
     for (int k = 0; k < kPre; ++k)
-      if (k < n) y[k] = load_cg(rows + slot(k) * 32);
+      if (k1 + k * share < n) y[k] = load_cg(rows + slot(k1 + k * share) * 32);
     const float m = lane < n ? x.x : -INFINITY;
     float top = m;
 #pragma unroll
@@ -301,17 +304,30 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, int r0, uint32_t
     float sum = lane < n ? f * x.y : 0.f;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    for (int k0 = 0; k0 < n; k0 += kPre) {
+    for (int k0 = k1; k0 < n; k0 += kPre * share) {
 #pragma unroll
       for (int k = 0; k < kPre; ++k) {
-        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) % 32);
-        if (k0 + k < n)
+        const int at = k0 + k * share;
+        const float w = __shfl_sync(0xffffffffu, f, at % 32);
+        if (at < n)
 #pragma unroll
           for (int e = 0; e < V; ++e) acc[e] = fmaf(w, y[k].get(e), acc[e]);
       }
 #pragma unroll
-      for (int k = 0; k < kPre; ++k)
-        if (k0 + kPre + k < n) y[k] = load_cg(rows + slot(k0 + kPre + k) * 32);
+      for (int k = 0; k < kPre; ++k) {
+        const int at = k0 + (kPre + k) * share;
+        if (at < n) y[k] = load_cg(rows + slot(at) * 32);
+      }
+    }
+    if (share > 1) {   // uniform: every warp is here once
+      if (k1 > 0)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sums[(warp * 32 + lane) * V + e] = acc[e];
+      __syncthreads();
+      if (k1 > 0) break;
+      for (int k = 1; k < share; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += sums[((warp + k) * 32 + lane) * V + e];
     }
     if (out) {
       const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
@@ -364,10 +380,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   const T* pool = static_cast<const T*>(a.c.pool);
   const long long v_off = (long long)a.c.page_size * a.c.H * D;
 
+  // A piece's queries, and its new key and value where it holds the new
+  // token: 16 bytes a thread and round, requested a piece ahead.
+  constexpr int kQ = kRows * S::kChunks / kThreads > 0 ? kRows * S::kChunks / kThreads : 1;
+  uint4 raw[kQ], raw_new = make_uint4(0, 0, 0, 0);
+  int new_page = -1, new_pos = -1;
+  auto request = [&](const Piece& p) {
+    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + q0 * a.q.head_stride;
+#pragma unroll
+    for (int x = 0; x < kQ; ++x) {
+      const int i = (x * kThreads + tid) / S::kChunks, chunk = tid % S::kChunks;
+      raw[x] = i < heads ? *reinterpret_cast<const uint4*>(q + i * a.q.head_stride + chunk * 8)
+                                                : make_uint4(0, 0, 0, 0);
+    }
+    if (kFused) {
+      if (a.positions) new_pos = __ldg(a.positions + p.seq);
+      if (p.tok1 == p.len) {
+        new_page = __ldg(a.c.tables + p.seq * a.c.table_stride + page_of(a.c, p.len - 1));
+        if (tid < 2 * S::kChunks) {
+          const RowsIn& from = tid < S::kChunks ? a.k : a.v;
+          raw_new = *reinterpret_cast<const uint4*>(static_cast<const T*>(from.p) + p.seq * from.token_stride +
+                                                    h * from.head_stride + tid % S::kChunks * 8);
+        }
+      }
+    }
+  };
+
+  Split ahead = work;
+  Piece p;
+  bool more = next_piece(a, rank, work, p);
+  if (more) request(p);
+
   // The loads' side runs kStages - 1 steps ahead of the products', over the
   // ends of units. Step i of a warp in a piece: tokens
   // [tok0 + (i kWarps + warp) kStep, + kStep).
-  Split ahead = work;
   constexpr int kPerPass = 32 / S::kChunks;   // rows of a pass
   const int chunk = lane % S::kChunks;
   const long long row_size = (long long)a.c.H * D;
@@ -421,41 +467,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     cp_async_commit();
   }
 
-  // A piece's queries, and its new key and value where it holds the new
-  // token: 16 bytes a thread and round, requested a piece ahead.
-  constexpr int kQ = kRows * S::kChunks / kThreads > 0 ? kRows * S::kChunks / kThreads : 1;
-  uint4 raw[kQ], raw_new = make_uint4(0, 0, 0, 0);
-  int new_page = -1, new_pos = -1;
-  auto request = [&](const Piece& p) {
-    const T* q = static_cast<const T*>(a.q.p) + p.seq * a.q.token_stride + q0 * a.q.head_stride;
-#pragma unroll
-    for (int x = 0; x < kQ; ++x) {
-      const int i = (x * kThreads + tid) / S::kChunks, chunk = tid % S::kChunks;
-      raw[x] = i < heads ? *reinterpret_cast<const uint4*>(q + i * a.q.head_stride + chunk * 8)
-                                                : make_uint4(0, 0, 0, 0);
-    }
-    if (kFused) {
-      if (a.positions) new_pos = __ldg(a.positions + p.seq);
-      if (p.tok1 == p.len) {
-        new_page = __ldg(a.c.tables + p.seq * a.c.table_stride + page_of(a.c, p.len - 1));
-        if (tid < 2 * S::kChunks) {
-          const RowsIn& from = tid < S::kChunks ? a.k : a.v;
-          raw_new = *reinterpret_cast<const uint4*>(static_cast<const T*>(from.p) + p.seq * from.token_stride +
-                                                    h * from.head_stride + tid % S::kChunks * 8);
-        }
-      }
-    }
-  };
-
   // The thread's pair of a head's values, in every piece.
   int e0 = 0, e1 = 0;
   const bool on = kFused && rope_pair(a.rope, tid % (D / 2), e0, e1);
   const uint64_t turn = on ? a.rope.turn[tid % (D / 2)] : 0;
 
   int stage = 0;
-  Piece p;
-  bool more = next_piece(a, rank, work, p);
-  if (more) request(p);
   while (more) {
     const int tok0 = p.tok0 + warp * S::kStep, tok1 = p.tok1;
     const bool has_new = kFused && tok1 == p.len;   // the new token's row lies in this piece
@@ -720,13 +737,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       }
       __syncthreads();
       bool last = s_last;
-      if (last) join_parts<D, T, kRows>(a, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
+      if (last) join_parts<D, T, kRows>(a, wo, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
       if (last && two) {
         __syncthreads();
         if (tid == 0) s_last = arrive_last(a.counters + 2 * gridDim.x + part_slot(a, p.r0, 0, unit), groups);
         __syncthreads();
         last = s_last;
-        if (last) join_parts<D, T, kRows>(a, p.r0, unit, 0, kGroup, groups, heads, to);
+        if (last) join_parts<D, T, kRows>(a, wo, p.r0, unit, 0, kGroup, groups, heads, to);
       }
     }
     p = next;
