@@ -16,8 +16,8 @@
 namespace pkv {
 
 namespace {
-constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;
+constexpr int kThreads = 128;
+constexpr int kCtasPerSm = 8;
 constexpr int kAhead = 2;         // rows in flight per thread, keys and values
 constexpr int kMaxTokens = 16;    // tokens of a block
 constexpr int kMaxSeqs = 1024;    // sequences whose cu_new and lengths are kept in shared memory
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_tokens_kernel(con
     }
     __syncthreads();
   }
+  int j = -1, page = -1;   // of the thread's token: its index in its sequence (-1: not written), and that page
   if (threadIdx.x < tokens) {
     const int i = threadIdx.x, t = first + i;
     const int32_t* cu = kept ? s_cu : a.cu_new;
@@ -93,37 +94,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_tokens_kernel(con
         }
       }
     }
-    int at = -1, pos = 0;
+    int pos = 0;
     if (s < n) {
       const int raw = kept ? s_len[s] : __ldg(a.c.lens + s), len = held(a.c, raw);
-      const int j = len - back;
-      bool bad = raw != len;
-      if (j >= 0) {
-        at = token_row(a.c, s, j);
-        bad |= at < 0;
-      } else if (len > 0) {
-        bad = true;   // more new tokens than the sequence holds (len 0: an unused row)
-      }
-      if (bad) {
-        at = -1;
-        raise_error(a.c.error, kErrIndex);
-      }
+      j = len - back;
       pos = a.positions ? __ldg(a.positions + t) : j;
+      if (raw != len || (j < 0 && len > 0)) {   // more new tokens than the sequence holds (len 0: an unused row)
+        raise_error(a.c.error, kErrIndex);
+        j = -1;
+      }
+      if (j >= 0) page = __ldg(a.c.tables + s * a.c.table_stride + page_of(a.c, j));
     }
-    s_row[i] = at;
     s_pos[i] = pos;
   }
   __syncthreads();
+  // The angles, while the pages are on their way.
   const int pairs = a.rope.rot / 2;
-  if (pairs > 0) {
-    for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-      const int t = divided(i, a.pair_mul, a.pair_shift), p = i - t * pairs;
-      float c, sn;
-      rope_angle(a.rope.turn[p], s_pos[t], a.rope.amplitude, c, sn);
-      s_angle[angle_at<V>(units, t, p)] = make_float2(c, sn);
-    }
-    __syncthreads();
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int t = divided(i, a.pair_mul, a.pair_shift), p = i - t * pairs;
+    float c, sn;
+    rope_angle(a.rope.turn[p], s_pos[t], a.rope.amplitude, c, sn);
+    s_angle[angle_at<V>(units, t, p)] = make_float2(c, sn);
   }
+  if (threadIdx.x < tokens) {
+    const int at = j >= 0 ? row_in(a.c, page, j) : -1;
+    if (j >= 0 && at < 0) raise_error(a.c.error, kErrIndex);
+    s_row[threadIdx.x] = at;
+  }
+  __syncthreads();
   const long long v_off = (long long)a.c.page_size * a.c.H * a.c.D;
   for (int r0 = slot; r0 < rows; r0 += kAhead * slots) {
 #pragma unroll
