@@ -540,7 +540,8 @@ int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, s
  * them). q [n_seqs, q_heads, D], rows on 16-byte boundaries; out
  * [n_seqs, q_heads, D] contiguous, in the pool's dtype. scale 0 is 1/sqrt(D).
  * Rows of length 0 give zeros. fp32 statistics and sums, rounded once; equal
- * inputs give equal bits. workspace: of kv_decode_workspace_init; one that was
+ * inputs give equal bits. What the pool holds outside of the tokens seen does
+ * not count; an infinity or NaN among them makes its outputs not finite. workspace: of kv_decode_workspace_init; one that was
  * not prepared raises the error word, and sequences split over several CTAs
  * are then not written. tables and lens must not change while a call runs.
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY (workspace),

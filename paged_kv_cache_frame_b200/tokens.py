@@ -281,7 +281,10 @@ class Rope:
     def rotate(self, x, positions, out=None, inverse=False, stream=None):
         """x [tokens, heads, head_dim] (bfloat16, float16 or float32; the
         last dimension dense) rotated at positions [tokens] (int32), into
-        `out` if given (x itself, or apart from it). Differentiable in x."""
+        `out` if given (x itself, or apart from it). Differentiable in x, the
+        gradient too. A captured backward pass belongs in one capture with its
+        forward, through torch.autograd.grad: a captured .backward() meets the
+        streams of any eager graph of the same leaves that is still alive."""
         if (x.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
             if out is not None or stream is not None:
                 raise ValueError("rotate: out and stream are not for a call that records a gradient "
@@ -296,8 +299,10 @@ class PagedTokens:
     pool: [max_pages, 2, page_size, heads, head_dim], bfloat16 or float16,
     head_dim 64 or 128. tables: [n_seqs, width] int32 page ids. lens:
     [n_seqs] int32, tokens of each sequence, the new ones included; 0 marks an
-    unused row. Both may be changed on the device between calls, and replayed
-    captures read them anew."""
+    unused row. Both may be changed in place between calls, and replayed
+    captures read them anew. The object holds the device's error word: keep it
+    as long as a captured call may be replayed, and order its use on another
+    stream behind its construction, as for any tensor."""
 
     def __init__(self, pool, tables, lens):
         _bind_torch()
@@ -313,7 +318,7 @@ class PagedTokens:
         self.n_seqs, width = tables.shape
         _check(tables, "tables", (self.n_seqs, width), torch.int32, pool.device, contiguous=False)
         _check(lens, "lens", (self.n_seqs,), torch.int32, pool.device)
-        self.pool, self.tables, self.lens = pool, tables, lens
+        self._pool, self._tables, self._lens = pool, tables, lens
         self.max_pages, _, self.page_size, self.H, self.D = pool.shape
         self._dtype, self._device = pool.dtype, pool.device
         self.error = torch.zeros(1, dtype=torch.int32, device=pool.device)
@@ -324,6 +329,11 @@ class PagedTokens:
         self._lib = capi.lib()
         self._bytes = {}        # query heads -> workspace bytes
         self._workspaces = {}   # (stream, query heads) -> the workspace of eager calls there
+
+    # The library holds their addresses: other tensors need another object.
+    pool = property(lambda self: self._pool)
+    tables = property(lambda self: self._tables)
+    lens = property(lambda self: self._lens)
 
     @classmethod
     def of_plan(cls, plan, block, streams=None):

@@ -276,6 +276,60 @@ def test_decode_many_sequences(pkv, d, dtype):
     b.cache.check_device()
 
 
+@pytest.mark.parametrize("fused", [False, True])
+def test_as_many_sequences_as_a_call_takes_and_coarse_tiles(pkv, fused):
+    """16384 sequences whose tables could name 2^24 tokens each: the split counts in coarser tiles. The sequences share
+    four pages (none that a new token goes to, but for one's own last)."""
+    n, page, width, g = 16384, 65536, 256, gen(26)
+    pool = randn((5, 2, page, 1, 64), torch.bfloat16, g)
+    lens = torch.ones(n, dtype=torch.int32)
+    some = {5: 0, 100: 300, 9000: 257, 9001: 0, 16383: 40000}
+    for s, x in some.items():
+        lens[s] = x
+    tables = torch.full((n, width), -1, dtype=torch.int32)
+    tables[:, 0] = torch.arange(n) % 4
+    if fused:                                       # only one sequence appends: the others are unused
+        tables[16383, 0] = 4
+        lens[:16383] = 0
+    cache = pkv.PagedTokens(pool, tables.cuda(), lens.cuda())
+    q = randn((n, 2, 64), torch.bfloat16, g)
+    if fused:
+        k, v = randn((n, 1, 64), torch.bfloat16, g), randn((n, 1, 64), torch.bfloat16, g)
+        out = cache.decode_append(k, v, q)
+        assert torch.equal(pool[4, 0, 39999], k[16383]) and torch.equal(pool[4, 1, 39999], v[16383])
+    else:
+        out = cache.decode(q)
+    cache.check_device()
+    b = Batch.__new__(Batch)
+    b.d = 64
+    for s in some:
+        b.lens = [int(lens[s])]
+        p = int(tables[s, 0])
+        kv = pool[p, :, :b.lens[0]].double()
+        assert_attended(out[s:s + 1], b, q[s:s + 1], kv=[(kv[0], kv[1])])
+    one = torch.ones(n, dtype=torch.bool)
+    one[list(some)] = False
+    if fused:
+        assert (out[one.cuda()] == 0).all()
+    else:                                           # one token: its value, to the bit
+        want = pool[tables[:, 0].cuda().long(), 1, 0].expand(n, 2, 64)
+        assert torch.equal(out[one.cuda()], want[one.cuda()])
+
+
+@pytest.mark.parametrize("hkv,g", [(300, 1), (149, 2), (148, 1), (3, 1600)])
+def test_more_heads_than_the_gpu_has_room_for(pkv, hkv, g):
+    """Units that fill the GPU alone: a CTA each, and nothing to join."""
+    b = Batch(pkv, [700, 0, 33], hkv, 64, 40, "fp16", seed=27)
+    q = randn((3, hkv * g, 64), b.dtype, b.g)
+    assert_attended(b.cache.decode(q), b, q)
+    k, v = randn((3, hkv, 64), b.dtype, b.g), randn((3, hkv, 64), b.dtype, b.g)
+    before = b.pool.clone()
+    out = b.cache.decode_append(k, v, q)
+    assert_appended(b, before, [1, 1, 1], k, v, None)
+    assert_attended(out, b, q)
+    b.cache.check_device()
+
+
 def test_decode_nothing(pkv):
     b = Batch(pkv, [0, 0], 2, 64, 16, width=2)
     out = torch.full((2, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
@@ -677,6 +731,9 @@ def test_refused_calls(pkv):
     for call in bad:
         with pytest.raises(ValueError):
             call()
+    for name in ("pool", "tables", "lens"):         # the library holds their addresses
+        with pytest.raises(AttributeError):
+            setattr(b.cache, name, getattr(b.cache, name).clone())
     with pytest.raises(pkv.KVError) as e:
         b.cache.decode(q, workspace=ws)
     assert e.value.name == "CAPACITY"
