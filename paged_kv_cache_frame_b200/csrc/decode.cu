@@ -520,21 +520,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
     // Queries as B operands: heads lane / 4 of each block of 8, values
     // 16 k + (lane % 4) * 2 and the next, and those 8 further.
-    uint32_t qb[NT][D / 16][2], qlo[NT][kFused ? D / 16 : 1][2];
+    // Of two blocks the remainders stay in shared memory (where the queries
+    // as they came were), four registers' worth of a lane side by side.
+    constexpr bool kLowInSmem = kFused && NT == 2;
+    uint32_t qb[NT][D / 16][2], qlo[NT][kFused && !kLowInSmem ? D / 16 : 1][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t lo[NT][2];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int at = (n * 8 + lane / 4) * D + k * 16 + e * 8 + lane % 4 * 2;
-          if (kFused) {
+          if constexpr (kFused) {
             const float2 x = *reinterpret_cast<const float2*>(sf + at);
-            split2<T>(x.x, x.y, qb[n][k][e], qlo[n][k][e]);   // the rotated query is not rounded
+            split2<T>(x.x, x.y, qb[n][k][e], lo[n][e]);   // the rotated query is not rounded
+            if constexpr (!kLowInSmem) qlo[n][k][e] = lo[n][e];
           } else {
             qb[n][k][e] = reinterpret_cast<const uint32_t*>(sq)[at / 2];
           }
         }
+      if constexpr (kLowInSmem)
+        if (k % kWarps == warp) sq[k * 32 + lane] = make_uint4(lo[0][0], lo[0][1], lo[NT - 1][0], lo[NT - 1][1]);
+    }
+    if constexpr (kLowInSmem) __syncthreads();
 
     float o[NT][D / 16][4] = {};
     float m[NT][2], l[NT][2];
@@ -568,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       // S^T: rows are tokens lane / 4 and lane / 4 + 8 of each block, columns
       // heads (lane % 4) * 2 and the next. Even and odd products (and the
       // queries' remainders) in sums of their own: shorter chains.
-      constexpr int kSums = kFused ? 4 : 2;
+      constexpr int kTurns = NT == 1 ? 2 : 1;         // even and odd apart, where a block of heads does not do
+      constexpr int kSums = kFused ? 2 * kTurns : kTurns;
       float sc[S::kM][NT][4];
 #pragma unroll
       for (int b = 0; b < S::kM; ++b) {
@@ -578,18 +588,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
           uint32_t x[4];
           const int r = b * 16 + lane % 16;
           ldsm_x4(ks + r * (D * 2) + (((2 * k + lane / 16) ^ (r & 7)) << 4), x);
+          uint4 lows = make_uint4(0, 0, 0, 0);
+          if constexpr (kLowInSmem) lows = sq[k * 32 + lane];
+          auto low = [&](int n, int k, int e) {
+            if constexpr (kLowInSmem) return n ? (e ? lows.w : lows.z) : (e ? lows.y : lows.x);
+            else return qlo[n][k][e];
+          };
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_16816<kFP16>(part[n][k % 2], x, qb[n][k][0], qb[n][k][1]);
-            if (kFused) mma_16816<kFP16>(part[n][2 + k % 2], x, qlo[n][k][0], qlo[n][k][1]);
+            mma_16816<kFP16>(part[n][k % kTurns], x, qb[n][k][0], qb[n][k][1]);
+            if constexpr (kFused)
+              mma_16816<kFP16>(part[n][kTurns + k % kTurns], x, low(n, k, 0), low(n, k, 1));
           }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float x = part[n][0][e] + part[n][1][e];
-            if constexpr (kFused) x += part[n][2][e] + part[n][3][e];
+            float x = part[n][0][e];
+#pragma unroll
+            for (int t = 1; t < kSums; ++t) x += part[n][t][e];
             sc[b][n][e] = x * a.scale_log2;
           }
       }
@@ -652,16 +670,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
             pl[n][e] = movmatrix_t(lo);
           }
         }
+        // A few blocks of values at a time, first with P, then with its
+        // remainder: no product waits for the one before it.
+        constexpr int kBlocks = 4 / NT;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t x[4];
+        for (int k0 = 0; k0 < D / 16; k0 += kBlocks) {
+          uint32_t x[kBlocks][4];
           const int r = b * 16 + lane % 8 + lane / 16 * 8;
-          ldsm_x4_t(vs + r * (D * 2) + (((2 * k + (lane / 8 & 1)) ^ (r & 7)) << 4), x);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16816<kFP16>(o[n][k], x, ph[n][0], ph[n][1]);
-            mma_16816<kFP16>(o[n][k], x, pl[n][0], pl[n][1]);
-          }
+          for (int k = 0; k < kBlocks; ++k)
+            ldsm_x4_t(vs + r * (D * 2) + (((2 * (k0 + k) + (lane / 8 & 1)) ^ (r & 7)) << 4), x[k]);
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816<kFP16>(o[n][k0 + k], x[k], ph[n][0], ph[n][1]);
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816<kFP16>(o[n][k0 + k], x[k], pl[n][0], pl[n][1]);
         }
       }
     }
