@@ -93,7 +93,7 @@ _IP = ctypes.POINTER(ctypes.c_int)
 _D = ctypes.c_double
 _DP = ctypes.POINTER(ctypes.c_double)
 _F = ctypes.c_float
-_ROWS = ctypes.POINTER(kv_rows)
+_ROWS = _P      # a kv_rows, by address or as its packed bytes
 _TOKENS = ctypes.POINTER(kv_tokens)
 
 # name -> (restype, argtypes)

@@ -18,12 +18,12 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 from . import capi
 from .capi import (KV_BF16, KV_FP16, KV_FP32, KV_ROPE_HALF, KV_ROPE_INTERLEAVED, KV_ROPE_LINEAR, KV_ROPE_NONE,
                    KV_ROPE_NTK, KV_ROPE_YARN)
 
-_kv_rows = capi.kv_rows
 LAYOUTS = {"half": KV_ROPE_HALF, "interleaved": KV_ROPE_INTERLEAVED}
 SCALINGS = {"none": KV_ROPE_NONE, "linear": KV_ROPE_LINEAR, "ntk": KV_ROPE_NTK, "yarn": KV_ROPE_YARN}
 
@@ -60,16 +60,20 @@ def kv_rope_get(rope) -> dict:
             "theta": list(theta[: rot.value // 2])}
 
 
+def _by_address(rows):
+    return ctypes.byref(rows) if isinstance(rows, capi.kv_rows) else rows
+
+
 def kv_rotate(rope, x, out, positions, n_tokens, n_heads, head_dim, dtype, inverse=False, stream=None) -> None:
     """x and out: capi.kv_rows; positions: a device address."""
-    capi.check(capi.lib().kv_rotate(rope, x, out, positions, n_tokens, n_heads, head_dim, dtype, int(bool(inverse)),
-                                    stream), "kv_rotate")
+    capi.check(capi.lib().kv_rotate(rope, _by_address(x), _by_address(out), positions, n_tokens, n_heads, head_dim, dtype,
+                                    int(bool(inverse)), stream), "kv_rotate")
 
 
 def kv_append_tokens(tokens, k, v, n_tokens, cu_new=None, rope=None, positions=None, stream=None) -> None:
     """tokens: capi.kv_tokens; k and v: capi.kv_rows; cu_new and positions: device addresses."""
-    capi.check(capi.lib().kv_append_tokens(tokens, k, v, n_tokens, cu_new, rope, positions, stream),
-               "kv_append_tokens")
+    capi.check(capi.lib().kv_append_tokens(tokens, _by_address(k), _by_address(v), n_tokens, cu_new, rope, positions,
+                                           stream), "kv_append_tokens")
 
 
 def kv_decode_workspace_bytes(tokens, q_heads) -> int:
@@ -82,14 +86,15 @@ def kv_decode_workspace_init(tokens, q_heads, workspace, workspace_bytes, stream
 
 
 def kv_decode(tokens, q, q_heads, scale, window, out, workspace, workspace_bytes, stream=None) -> None:
-    capi.check(capi.lib().kv_decode(tokens, q, q_heads, scale, window, out, workspace, workspace_bytes, stream),
+    capi.check(capi.lib().kv_decode(tokens, _by_address(q), q_heads, scale, window, out, workspace, workspace_bytes, stream),
                "kv_decode")
 
 
 def kv_decode_append(tokens, k, v, q, q_heads, rope, positions, scale, window, out, workspace, workspace_bytes,
                      stream=None) -> None:
-    capi.check(capi.lib().kv_decode_append(tokens, k, v, q, q_heads, rope, positions, scale, window, out, workspace,
-                                           workspace_bytes, stream), "kv_decode_append")
+    capi.check(capi.lib().kv_decode_append(tokens, _by_address(k), _by_address(v), _by_address(q), q_heads, rope,
+                                           positions, scale, window, out, workspace, workspace_bytes, stream),
+               "kv_decode_append")
 
 
 def kv_tokens_check(tokens, stream=None) -> None:
@@ -134,12 +139,15 @@ def _no_gradient(*named):
                              "(detach it or call under torch.no_grad)")
 
 
+_pack_rows = struct.Struct("@Pqq").pack    # a kv_rows
+
+
 def _rows(x):
-    """kv_rows of a [n, heads, head_dim] tensor; the stride of a dimension of
-    one element says nothing and is 0."""
+    """The kv_rows of a [n, heads, head_dim] tensor, packed; the stride of a
+    dimension of one element says nothing and is 0."""
     n, h, _ = x.shape
     t, s, _ = x.stride()
-    return _kv_rows(x.data_ptr(), t if n > 1 else 0, s if h > 1 else 0)
+    return _pack_rows(x.data_ptr(), t if n > 1 else 0, s if h > 1 else 0)
 
 
 class _On:
