@@ -15,7 +15,7 @@
 // with each head's tokens cut elsewhere). The sequences are cut into tiles.
 // Every CTA works its own part of the split out from the lengths, which are
 // read on the device, so a captured launch serves growing sequences:
-//   - while cutting every sequence into parts of at most kPartTiles tiles
+//   - while cutting every sequence into parts of at most part_tiles tiles
 //     gives no more parts than ranks, each part is a rank's: short sequences
 //     stay whole, and nothing is joined that would not pay for it;
 //   - else all sequences' tiles (and kSeqCost more each, for what a sequence
@@ -27,7 +27,7 @@
 // that is: results do not depend on timing, and no CTA waits for another.
 // More than kJoin parts are joined in two rounds, kGroup neighbours first.
 //
-// In a CTA each warp takes every kWarps-th step of kStep tokens and keeps a
+// In a CTA each of the W warps takes every W-th step of kStep tokens and keeps a
 // running max, sum and O of its own; no warp waits for another until the end
 // of the sequence. Token rows are gathered by 16-byte asynchronous copies into a
 // ring per warp (rows past the end are zero-filled and masked, so what the
@@ -42,8 +42,10 @@
 // measured 2 clk per mma and SM these take about a fifth of the time the
 // bytes need. P is fed as a sum of two 16-bit values (its rounding and the
 // rest): rounding P alone would add an error as large as the output's own.
+#pragma once
 #include <limits.h>
 
+#include "decode_shape.h"
 #include "launch.cuh"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -53,24 +55,22 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 8.f;   // growth of a score, in powers of two, that the running max lets pass
-constexpr int kPartTiles = 3;   // tiles (32 KB of K and V each) that are not worth a join
-constexpr int kSeqCost = 3;     // a sequence's own cost in tiles
 constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
 constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
-template <int D>
+template <int D, int NT, bool kFused, int W>
 struct Shape {
-  static constexpr int kM = D == 64 ? 2 : 1;            // 16-token blocks of a step
-  static constexpr int kStep = 16 * kM;                 // tokens a warp takes at a time (8 KB of K and V)
-  static constexpr int kStride = kStep * kWarps;        // tokens of a step of all warps, and of the finest tile
-  static constexpr int kStages = 3;
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kCtasPerSm = decode_ctas_per_sm(8 * NT, kFused, W);
+  static constexpr int kStep = decode_step(D);
+  static constexpr int kM = kStep / 16;                 // 16-token blocks of a step
+  static constexpr int kStride = kStep * W;             // tokens of a step of all warps
+  static constexpr int kStages = decode_stages(8 * NT, kFused, W);
   static constexpr int kHalf = kStep * D * 2;           // K (or V) bytes of a stage
-  static constexpr int kRing = kWarps * kStages * 2 * kHalf;
+  static constexpr int kRing = W * kStages * 2 * kHalf;
   static constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
+  static constexpr int kBlock = D == 128 && kCtasPerSm == 3 ? 4 : 8;   // heads whose O the warps join at a time
 };
 
 // (a, b) as packed 16-bit values and the packed remainders.
@@ -99,24 +99,32 @@ __device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, int len) {
 
 // Shared memory behind the rings. A unit's queries (as they come, and
 // rotated) take the place of the warps' O: never at once.
-template <int D, int NT>
+template <int D, int NT, bool kFused, int W>
 struct Smem {
+  using S = Shape<D, NT, kFused, W>;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kOffO = Shape<D>::kRing;                        // [warp][8 heads][D] fp32, one block of 8 at a time
-  static constexpr int kOffMl = kOffO + kWarps * 8 * D * 4;            // [warp][8 heads] (max, sum)
-  static constexpr int kOffNew = kOffMl + kWarps * 8 * 8;              // fused: new key and value [2][D]
+  static constexpr int kO = W * S::kBlock * D * 4;
+  static constexpr int kOffO = S::kRing;                               // [warp][kBlock heads][D] fp32
+  static constexpr int kOffMl = kOffO + kO;                            // [warp][kBlock heads] (max, sum)
+  static constexpr int kOffNew = kOffMl + W * S::kBlock * 8;           // fused: new key and value [2][D]
   static constexpr int kBytes = kOffNew + 2 * D * 2;
   static constexpr int kOffTurned = kOffO + kRows * D * 2;             // queries [row][D] fp32, behind them as they came
-  static_assert(kRows * D * 6 <= kWarps * 8 * D * 4, "the queries fit the warps' O");
+  static_assert(kRows * D * 6 <= kO, "the queries fit the warps' O");
   // An SM has 228 KB, of which every CTA takes 1 KB and its static part besides.
-  static_assert(kCtasPerSm * (kBytes + 1024 + 128) <= 228 * 1024, "the CTAs of an SM fit");
+  static_assert(S::kCtasPerSm * (kBytes + 1024 + 128) <= 228 * 1024, "the CTAs of an SM fit");
+};
+
+// A lane's remainders of the queries in one product.
+template <int NT>
+struct alignas(8 * NT) Low {
+  uint32_t w[NT][2];
 };
 
 // Element d of row i of a warp's O block: row i shifted by 4 i floats, so
 // that no two lanes of an accumulator's store share a bank.
-template <int D>
+template <int D, int kBlock>
 __device__ __forceinline__ int o_at(int w, int i, int d) {
-  return (w * 8 + i) * D + ((d + 4 * i) & (D - 1));
+  return (w * kBlock + i) * D + ((d + 4 * i) & (D - 1));
 }
 
 // Pair p (of D / 2) of a head in the rotation's order: its two elements, and
@@ -161,7 +169,9 @@ struct Piece {
 __device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
   return s < a.c.n_seqs ? __ldg(a.c.lens + s) : 0;
 }
-__device__ __forceinline__ uint32_t parts_of(uint32_t tiles) { return (tiles + kPartTiles - 1) / kPartTiles; }
+__device__ __forceinline__ uint32_t parts_of(const DecodeArgs& a, uint32_t tiles) {
+  return (tiles + a.part_tiles - 1) / a.part_tiles;
+}
 
 // On to the next sequence's places.
 __device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
@@ -169,7 +179,7 @@ __device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
   l.len = held(a.c, l.later);
   l.later = raw_len(a, l.seq + 1);
   l.tiles = tiles_of(a, l.len);
-  l.size = l.by_parts ? parts_of(l.tiles) : l.tiles ? l.tiles + kSeqCost : 0;
+  l.size = l.by_parts ? parts_of(a, l.tiles) : l.tiles ? l.tiles + kSeqCost : 0;
   l.at = 0;
 }
 
@@ -179,7 +189,7 @@ __device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t rank, S
     if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
     uint32_t tile0, tile1;
     if (l.by_parts) {
-      tile0 = l.tiles * l.at / l.size;   // tiles <= kPartTiles * ranks here
+      tile0 = l.tiles * l.at / l.size;   // tiles <= part_tiles * ranks here
       tile1 = l.tiles * (l.at + 1) / l.size;
       p.r0 = l.t - l.at;
       p.parts = l.size;
@@ -215,7 +225,7 @@ __device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t rank) {
   unsigned long long mine = 0;   // places of the line below, parts above; both stay below 2^31
   for (int s = s0; s < s1; ++s) {
     const uint32_t tiles = tiles_of(a, seq_len(a.c, s));
-    mine += (unsigned long long)parts_of(tiles) << 32 | (tiles ? tiles + kSeqCost : 0);
+    mine += (unsigned long long)parts_of(a, tiles) << 32 | (tiles ? tiles + kSeqCost : 0);
   }
   unsigned long long upto = mine;
 #pragma unroll
@@ -273,21 +283,22 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
 // Joins parts p0, p0 + step, ... (n of at most 32) of the sequence begun by
 // rank r0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
 // writes O / l to `out` (the unit's first query row of the sequence), others the part in the
-// first one's place. A warp takes a query head at a time (of one or two
-// heads all warps, each some of the parts, added up in `sums`), a lane a
+// first one's place. A warp takes a query head at a time (of fewer heads
+// than warps, if they divide these, several warps some of its parts each, added
+// up in `sums`), a lane a
 // part's weight, then all lanes the parts' rows with kPre of them in flight,
 // the first before the weights are known. All threads of the CTA.
-template <int D, typename T, int kRows>
+template <int D, typename T, int kRows, int W>
 __device__ __forceinline__ void join_parts(const DecodeArgs& a, float* sums, int r0, uint32_t unit, int p0, int step, int n,
                                            int heads, T* out) {
   constexpr int V = D / 32;    // values of a lane
   constexpr int kPre = 8;
   using P = Pack<float, V>;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int share = heads == 1 ? kWarps : heads == 2 ? kWarps / 2 : 1;   // warps of a head
+  const int share = W % heads == 0 ? W / heads : 1;                      // warps of a head
   const int k1 = warp % share;                                           // this warp's parts: k1, k1 + share, ...
   auto slot = [&](int k) { return part_slot(a, r0, p0 + k * step, unit) * kRows; };
-  for (int i = warp / share; i < heads; i += kWarps / share) {
+  for (int i = warp / share; i < heads; i += W / share) {
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + i;
     P* rows = reinterpret_cast<P*>(a.part_o) + i * 32 + lane;
     const float2 x = __ldcg(ml + slot(min(lane, n - 1)));
@@ -347,10 +358,12 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, float* sums, int
 
 }  // namespace
 
-template <int D, typename T, int NT, bool kFused>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using S = Shape<D>;
-  using M = Smem<D, NT>;
+template <int D, typename T, int NT, bool kFused, int W>
+__global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT, kFused, W>::kCtasPerSm)
+    decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using S = Shape<D, NT, kFused, W>;
+  using M = Smem<D, NT, kFused, W>;
+  constexpr int kThreads = S::kThreads;
   constexpr int kRows = M::kRows;
   constexpr bool kFP16 = kIsFp16<T>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 
   // The loads' side runs kStages - 1 steps ahead of the products', over the
   // ends of units. Step i of a warp in a piece: tokens
-  // [tok0 + (i kWarps + warp) kStep, + kStep).
+  // [tok0 + (i W + warp) kStep, + kStep).
   constexpr int kPerPass = 32 / S::kChunks;   // rows of a pass
   const int chunk = lane % S::kChunks;
   const long long row_size = (long long)a.c.H * D;
@@ -521,8 +534,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     // Queries as B operands: heads lane / 4 of each block of 8, values
     // 16 k + (lane % 4) * 2 and the next, and those 8 further.
     // Of two blocks the remainders stay in shared memory (where the queries
-    // as they came were), four registers' worth of a lane side by side.
+    // as they came were), a lane's of a product side by side: registers.
     constexpr bool kLowInSmem = kFused && NT == 2;
+    Low<NT>* const low_at = reinterpret_cast<Low<NT>*>(sq);
     uint32_t qb[NT][D / 16][2], qlo[NT][kFused && !kLowInSmem ? D / 16 : 1][2];
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -541,7 +555,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
           }
         }
       if constexpr (kLowInSmem)
-        if (k % kWarps == warp) sq[k * 32 + lane] = make_uint4(lo[0][0], lo[0][1], lo[NT - 1][0], lo[NT - 1][1]);
+        if (k % W == warp) {
+          Low<NT> x;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x.w[n][0] = lo[n][0], x.w[n][1] = lo[n][1];
+          low_at[k * 32 + lane] = x;
+        }
     }
     if constexpr (kLowInSmem) __syncthreads();
 
@@ -588,10 +607,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
           uint32_t x[4];
           const int r = b * 16 + lane % 16;
           ldsm_x4(ks + r * (D * 2) + (((2 * k + lane / 16) ^ (r & 7)) << 4), x);
-          uint4 lows = make_uint4(0, 0, 0, 0);
-          if constexpr (kLowInSmem) lows = sq[k * 32 + lane];
+          Low<NT> lows;
+          if constexpr (kLowInSmem) lows = low_at[k * 32 + lane];
           auto low = [&](int n, int k, int e) {
-            if constexpr (kLowInSmem) return n ? (e ? lows.w : lows.z) : (e ? lows.y : lows.x);
+            if constexpr (kLowInSmem) return lows.w[n][e];
             else return qlo[n][k][e];
           };
 #pragma unroll
@@ -698,53 +717,62 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
 
-    // Join the warps in shared memory, a block of 8 heads at a time.
+    // Join the warps in shared memory, a block of heads at a time.
     float* wo = reinterpret_cast<float*>(smem + M::kOffO);
     float* wml = reinterpret_cast<float*>(smem + M::kOffMl);
+    constexpr int kBlock = S::kBlock;
     const bool whole = p.parts == 1;
     const long long slot = part_slot(a, p.r0, rank - p.r0, unit);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (n > 0 && heads <= n * 8) break;
-      __syncthreads();   // what stood here has been read
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int block = 0; block < 8; block += kBlock) {
+        const int first = n * 8 + block;
+        if (first > 0 && heads <= first) break;
+        __syncthreads();   // what stood here has been read
+        const int i0 = lane % 4 * 2 - block;   // the lane's two heads, in the block or not
+        if (i0 >= 0 && i0 < kBlock) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          wo[o_at<D>(warp, lane % 4 * 2 + (e & 1), k * 16 + lane / 4 + (e >> 1) * 8)] = o[n][k][e];
-      if (lane < 4) {
+          for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<float2*>(wml + 2 * (warp * 8 + lane * 2 + c)) = make_float2(m[n][c], l[n][c]);
-      }
-      __syncthreads();
-      const int block = heads - n * 8 < 8 ? heads - n * 8 : 8;
-      for (int x = tid; x < block * (D / 2); x += kThreads) {
-        const int i = x / (D / 2), d = x % (D / 2) * 2;
-        float2 ml[kWarps];
-        float top = -INFINITY;
+            for (int e = 0; e < 4; ++e)
+              wo[o_at<D, kBlock>(warp, i0 + (e & 1), k * 16 + lane / 4 + (e >> 1) * 8)] = o[n][k][e];
+          if (lane < 4) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = *reinterpret_cast<const float2*>(wml + 2 * (w * 8 + i));
-          top = fmaxf(top, ml[w].x);
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<float2*>(wml + 2 * (warp * kBlock + i0 + c)) = make_float2(m[n][c], l[n][c]);
+          }
         }
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, a0 = 0.f, a1 = 0.f;
+        __syncthreads();
+        const int here = heads - first < kBlock ? heads - first : kBlock;
+        for (int x = tid; x < here * (D / 2); x += kThreads) {
+          const int i = x / (D / 2), d = x % (D / 2) * 2;
+          float2 ml[W];
+          float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2_approx(ml[w].x - ref);
-          const float2 y = *reinterpret_cast<const float2*>(wo + o_at<D>(w, i, d));
-          sum = fmaf(f, ml[w].y, sum);
-          a0 = fmaf(f, y.x, a0);
-          a1 = fmaf(f, y.y, a1);
-        }
-        const int row = n * 8 + i;
-        if (whole) {
-          const float r = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
-          *reinterpret_cast<uint32_t*>(out + ((long long)p.seq * q_heads + q0 + row) * D + d) = pack2<T>(a0 * r, a1 * r);
-        } else {
-          *reinterpret_cast<float2*>(a.part_o + (slot * kRows + row) * D + d) = make_float2(a0, a1);
-          if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + row) * 2) = make_float2(top, sum);
+          for (int w = 0; w < W; ++w) {
+            ml[w] = *reinterpret_cast<const float2*>(wml + 2 * (w * kBlock + i));
+            top = fmaxf(top, ml[w].x);
+          }
+          const float ref = top == -INFINITY ? 0.f : top;
+          float sum = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float f = ex2_approx(ml[w].x - ref);
+            const float2 y = *reinterpret_cast<const float2*>(wo + o_at<D, kBlock>(w, i, d));
+            sum = fmaf(f, ml[w].y, sum);
+            a0 = fmaf(f, y.x, a0);
+            a1 = fmaf(f, y.y, a1);
+          }
+          const int row = first + i;
+          if (whole) {
+            const float r = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
+            *reinterpret_cast<uint32_t*>(out + ((long long)p.seq * q_heads + q0 + row) * D + d) =
+                pack2<T>(a0 * r, a1 * r);
+          } else {
+            *reinterpret_cast<float2*>(a.part_o + (slot * kRows + row) * D + d) = make_float2(a0, a1);
+            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + row) * 2) = make_float2(top, sum);
+          }
         }
       }
     }
@@ -763,13 +791,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       }
       __syncthreads();
       bool last = s_last;
-      if (last) join_parts<D, T, kRows>(a, wo, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
+      if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
       if (last && two) {
         __syncthreads();
         if (tid == 0) s_last = arrive_last(a.counters + 2 * gridDim.x + part_slot(a, p.r0, 0, unit), groups);
         __syncthreads();
         last = s_last;
-        if (last) join_parts<D, T, kRows>(a, wo, p.r0, unit, 0, kGroup, groups, heads, to);
+        if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, 0, kGroup, groups, heads, to);
       }
     }
     p = next;
@@ -777,45 +805,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   cp_async_wait<0>();
 }
 
-int decode_rows(int group) { return group <= 8 ? 8 : 16; }
-
-// One, with a CTA a unit, where the units alone fill the GPU.
-int decode_ranks(int units, int num_sms) {
-  const int n = num_sms * kCtasPerSm / units;
-  return n > 1 ? n : 1;
-}
-
-// log2 of the tokens of a tile: the finest that keeps the line of the longest
-// possible sequences, every sequence's cost included, within 31 bits.
-int decode_tile_shift(int D, int n_seqs, long long most_tokens) {
-  int shift = D == 64 ? 7 : 6;
-  static_assert(Shape<64>::kStride == 128 && Shape<128>::kStride == 64, "the finest tile is a step of all warps");
-  while (((most_tokens >> shift) + 1 + kSeqCost) * n_seqs > INT_MAX) ++shift;
-  return shift;
-}
-
-template <int D, typename T, int NT, bool kFused>
-static cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
+template <int D, typename T, int NT, bool kFused, int W>
+cudaError_t launch_decode_shape(const DecodeArgs& a, cudaStream_t stream) {
   static std::atomic<uint8_t> done[kMaxDevices];
-  constexpr int kBytes = Smem<D, NT>::kBytes;
-  const cudaError_t e = ensure_dynamic_smem(decode_kernel<D, T, NT, kFused>, kBytes, done);
+  constexpr int kBytes = Smem<D, NT, kFused, W>::kBytes;
+  const cudaError_t e = ensure_dynamic_smem(decode_kernel<D, T, NT, kFused, W>, kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<D, T, NT, kFused>, dim3(a.ranks * a.units), dim3(kThreads), kBytes, stream, a);
+  return launch_pdl(decode_kernel<D, T, NT, kFused, W>, dim3(a.ranks * a.units), dim3(32 * W), kBytes, stream, a);
 }
 
-template <int D, typename T>
-static cudaError_t launch_shape(const DecodeArgs& a, bool fused, cudaStream_t stream) {
-  if (decode_rows(a.group) == 8) return fused ? launch<D, T, 1, true>(a, stream) : launch<D, T, 1, false>(a, stream);
-  return fused ? launch<D, T, 2, true>(a, stream) : launch<D, T, 2, false>(a, stream);
+template <int D, typename T, int NT>
+cudaError_t launch_decode_rows(const DecodeArgs& a, bool fused, cudaStream_t stream) {
+  if (a.warps == 8)
+    return fused ? launch_decode_shape<D, T, NT, true, 8>(a, stream) : launch_decode_shape<D, T, NT, false, 8>(a, stream);
+  return fused ? launch_decode_shape<D, T, NT, true, 4>(a, stream) : launch_decode_shape<D, T, NT, false, 4>(a, stream);
 }
 
-cudaError_t launch_decode(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream) {
-  if (a.c.n_seqs <= 0) return cudaSuccess;
-  if (a.c.D == 64)
-    return dtype == KV_FP16 ? launch_shape<64, __half>(a, fused, stream)
-                            : launch_shape<64, __nv_bfloat16>(a, fused, stream);
-  return dtype == KV_FP16 ? launch_shape<128, __half>(a, fused, stream)
-                          : launch_shape<128, __nv_bfloat16>(a, fused, stream);
+template <int D>
+cudaError_t launch_decode_dim(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream) {
+  const bool one = decode_rows(a.group) == 8;
+  if (dtype == KV_FP16)
+    return one ? launch_decode_rows<D, __half, 1>(a, fused, stream) : launch_decode_rows<D, __half, 2>(a, fused, stream);
+  return one ? launch_decode_rows<D, __nv_bfloat16, 1>(a, fused, stream)
+             : launch_decode_rows<D, __nv_bfloat16, 2>(a, fused, stream);
 }
 
 }  // namespace pkv

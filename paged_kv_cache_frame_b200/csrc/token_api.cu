@@ -9,6 +9,7 @@
 
 #include "../../include/kv.h"
 #include "api_error.h"
+#include "decode_shape.h"
 #include "launch.cuh"
 #include "page_divisor.h"
 #include "token_kernels.h"
@@ -89,24 +90,30 @@ int view_rope(const kv_rope_t* r, int head_dim, const std::string& who, pkv::Rop
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// [magic | arrival counters | the parts' maxima and sums | their outputs];
-// nothing is split where a unit has one CTA.
+// [magic | arrival counters | the parts' maxima and sums | their outputs], for
+// the largest of the shapes that a launch may have; nothing is split where a
+// unit has one CTA.
 struct DecodeLayout {
-  int units, ranks;
+  int units, rows, sms;
   size_t counters, off_counters, off_ml, off_o, total;
 };
 
 DecodeLayout decode_layout(const kv_tokens* c, int q_heads) {
-  const int group = q_heads / c->num_heads, rows = pkv::decode_rows(group);
+  const int group = q_heads / c->num_heads;
   DecodeLayout l;
-  l.units = c->num_heads * ((group + rows - 1) / rows);
-  l.ranks = pkv::decode_ranks(l.units, pkv::current_device_sms());
-  const size_t ctas = l.ranks > 1 ? (size_t)l.ranks * l.units : 0;
+  l.rows = pkv::decode_rows(group);
+  l.units = c->num_heads * ((group + l.rows - 1) / l.rows);
+  l.sms = pkv::current_device_sms();
+  size_t ctas = 0;
+  for (int shape = 0; shape < 4; ++shape) {
+    const int ranks = pkv::decode_ranks(l.units, l.rows, shape & 1, shape & 2 ? 8 : 4, l.sms);
+    if (ranks > 1 && (size_t)ranks * l.units > ctas) ctas = (size_t)ranks * l.units;
+  }
   l.counters = 4 * ctas * sizeof(uint32_t);
   l.off_counters = 256;
   l.off_ml = align256(l.off_counters + l.counters);
-  l.off_o = align256(l.off_ml + 2 * ctas * rows * 8);
-  l.total = align256(l.off_o + 2 * ctas * rows * c->head_dim * 4);
+  l.off_o = align256(l.off_ml + 2 * ctas * l.rows * 8);
+  l.total = align256(l.off_o + 2 * ctas * l.rows * c->head_dim * 4);
   return l;
 }
 
@@ -145,15 +152,17 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   a.counters = reinterpret_cast<uint32_t*>(ws + l.off_counters);
   a.part_ml = reinterpret_cast<float*>(ws + l.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + l.off_o);
-  const int rows = pkv::decode_rows(a.group);
-  a.head_groups = (a.group + rows - 1) / rows;
+  a.head_groups = l.units / c->num_heads;
   a.window = window;
   a.units = l.units;
-  a.ranks = l.ranks;
-  a.tile_shift = pkv::decode_tile_shift(c->head_dim, c->n_seqs, (long long)c->table_width * c->page_size);
+  a.warps = pkv::decode_warps(c->n_seqs, l.units, l.sms);
+  a.ranks = pkv::decode_ranks(l.units, l.rows, fused, a.warps, l.sms);
+  a.tile_shift = pkv::decode_tile_shift(c->head_dim, a.warps, c->n_seqs, (long long)c->table_width * c->page_size);
+  a.part_tiles = pkv::decode_part_tiles(a.warps);
   const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
   a.scale_log2 = (float)(s * 1.4426950408889634);
-  const cudaError_t e = pkv::launch_decode(a, c->dtype, fused, (cudaStream_t)stream);
+  const cudaError_t e = c->head_dim == 64 ? pkv::launch_decode_d64(a, c->dtype, fused, (cudaStream_t)stream)
+                                          : pkv::launch_decode_d128(a, c->dtype, fused, (cudaStream_t)stream);
   return e == cudaSuccess ? KV_OK : api_cuda_fail(e, (who + ": launch").c_str());
 }
 

@@ -72,17 +72,17 @@ struct DecodeArgs {
   int head_groups;            // groups of at most `rows` query heads a unit takes
   int window;                 // 0: the whole cache
   int units, ranks;           // CTAs: H * head_groups units, `ranks` of each
+  int warps;                  // of a CTA (decode_shape.h)
   int tile_shift;             // log2 of a tile's tokens
+  int part_tiles;             // tiles that are not worth a join
   float scale_log2;           // scale * log2(e)
   RopeTable rope;
 };
 
 cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_append_tokens(const AppendTokensArgs& a, int dtype, cudaStream_t stream);
-// Query heads one unit takes (8 or 16), CTAs of a unit, log2 of a tile's tokens.
-int decode_rows(int group);
-int decode_ranks(int units, int num_sms);
-int decode_tile_shift(int D, int n_seqs, long long most_tokens);
-cudaError_t launch_decode(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
+// One launch of a.ranks * a.units CTAs; heads of 64 or of 128 values.
+cudaError_t launch_decode_d64(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
+cudaError_t launch_decode_d128(const DecodeArgs& a, int dtype, bool fused, cudaStream_t stream);
 
 }  // namespace pkv

@@ -262,7 +262,7 @@ def test_sequence_search():
 
 
 JOIN, GROUP = 32, 16      # parts joined in one round, and neighbours joined first where there are more
-PART, COST = 3, 3         # tiles a part holds at most, a sequence's own cost in the line
+PART, COST = 3, 2         # tiles a part holds at most, a sequence's own cost in the line
 
 
 def split_pieces(tiles, ranks):
