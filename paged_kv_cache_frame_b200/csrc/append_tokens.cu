@@ -9,7 +9,10 @@
 // and 2u + 1 travel in the same thread. The first rows are on their way
 // meanwhile; cu_new and the lengths are fetched together into shared memory,
 // a thread a token searches there, and only its page is another load. Blocks
-// are made large enough for all of them to run at once.
+// are made large enough for all of them to run at once. Prompts of 9 sequences
+// (6930 tokens x 8 heads x 128, 57 MB, nothing in cache): 14.3 us, of which
+// the bytes need 8.7; with half as large blocks 15.5, with the search in
+// global memory 17.4. One token of 64 sequences: 2.8 us, a launch.
 #include "launch.cuh"
 #include "rope_unit.cuh"
 

@@ -4,9 +4,13 @@
 //
 // Bound by its bytes (each value read and written once). A block takes a few
 // tokens with all of their heads; its threads go through the (token, head)
-// rows with several rows' loads in flight, each thread at its own unit of V
+// rows with kAhead rows' loads in flight, each thread at its own unit of V
 // pairs. Sums of two products are in 32 bits, rounded once to the tensor's
-// type.
+// type. 8192 tokens x 40 heads x 128 values of 16 bits, inputs not in cache:
+// 29.7 us, 5.65 TB/s, 86% of a copy's rate (with the angles worked out by each
+// thread for itself 48.8, with blocks of 256 threads 31.1, with four rows in
+// flight and fewer blocks 30.6). 32-bit values, forward and gradient: 35.5 us
+// for 201 MB, 87%.
 #include "launch.cuh"
 #include "rope_unit.cuh"
 
