@@ -1,4 +1,5 @@
-"""Builds the in-tree shared library `_lib/libpkv.so` with nvcc for sm_100a.
+"""Builds the in-tree shared library `_lib/libpkv.so` with nvcc for sm_100a,
+and the token operators' Python binding `_lib/_tokens.so` against torch.
 
     python -m paged_kv_cache_frame_b200.build [--force] [--verbose]
 
@@ -23,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+BINDING_SRC = os.path.join(HERE, "binding", "tokens.cpp")
+BINDING = os.path.join(OUT_DIR, "_tokens.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -77,6 +80,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
     if not force and not ptxas_v and not _stale(LIB, srcs + headers()):
+        build_binding(force, verbose)
         return LIB
     if force:
         for o in glob.glob(os.path.join(OBJ_DIR, "*.o")):
@@ -92,7 +96,34 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> None:
+    """Compile the binding (if stale) with g++; it links to libpkv.so beside it."""
+    if not force and not _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "kv.h")]):
+        return
+    try:
+        import torch
+    except ImportError:   # the library itself does without; its Python objects do not
+        return
+    import sysconfig
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    tmp = BINDING + ".tmp"
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", BINDING_SRC, "-o", tmp]
+           + [x for p in inc for x in ("-isystem" if p != inc[-1] else "-I", p)]
+           + [f"-L{os.path.join(base, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+              f"-L{OUT_DIR}", "-lpkv", "-Wl,-rpath,$ORIGIN"])
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def main():

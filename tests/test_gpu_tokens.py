@@ -170,6 +170,17 @@ def test_rotate_gradient(pkv, layout, rot, dtype):
     assert_turned(dv, dt, pos, rope)
 
 
+def test_rotate_gradient_outlives_the_handle(pkv):
+    pos = torch.arange(9, device="cuda", dtype=torch.int32)
+    x = torch.randn(9, 2, 64, device="cuda", requires_grad=True)
+    rope = pkv.Rope(64, base=77.0)
+    y = rope.rotate(x, pos)
+    del rope
+    dy = torch.randn_like(y)
+    dx, = torch.autograd.grad(y, x, dy)
+    assert_turned(dx, dy, pos, pkv.Rope(64, base=77.0), -1)
+
+
 def test_rotate_gradient_sees_changed_positions(pkv):
     pos = torch.arange(4, device="cuda", dtype=torch.int32)
     x = torch.randn(4, 2, 64, device="cuda", requires_grad=True)
@@ -709,6 +720,33 @@ def test_streams(pkv):
     y = rope.rotate(q, pos, stream=s1)
     s1.synchronize()
     assert torch.equal(y, rope.rotate(q, pos))
+
+
+def test_threads(pkv):
+    """Calls of several host threads on one object, each on a stream of its own."""
+    import threading
+    b = Batch(pkv, [9000, 4000, 0, 70], 1, 64, 64, seed=28)
+    rope, pos = pkv.Rope(64), torch.arange(4, device="cuda", dtype=torch.int32)
+    qs = [randn((4, 3, 64), b.dtype, b.g) for _ in range(4)]
+    want = [(b.cache.decode(q), rope.rotate(q, pos)) for q in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = b.cache.decode(qs[i]), rope.rotate(qs[i], pos)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(x, y) for x, y in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    b.cache.check_device()
 
 
 def test_refused_calls(pkv):
