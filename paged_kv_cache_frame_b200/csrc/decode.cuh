@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   pdl_wait();      // the pool, the tables and the queries may come from earlier kernels
   pdl_trigger();
 
+  uint32_t magic = 0;
+  if (tid == 0) magic = __ldcg(a.ws_magic);
   Split work = split(a, rank);
   T* out = static_cast<T*>(a.out);
   const int q_heads = a.c.H * a.group;
@@ -434,9 +436,6 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   };
 
   Split ahead = work;
-  Piece p;
-  bool more = next_piece(a, rank, work, p);
-  if (more) request(p);
 
   // The loads' side runs kStages - 1 steps ahead of the products', over the
   // ends of units. Step i of a warp in a piece: tokens
@@ -446,8 +445,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   const long long row_size = (long long)a.c.H * D;
   const T* const src0 = pool + h * D + chunk * 8;                 // the lane's chunk of the head in row 0
   int l_seq = 0, l_len = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
-  int l_row = -1;                                                 // the lane's row of the next step, looked up ahead
-  bool l_ok = false;
+  int l_page = 0;                                                 // the lane's page of the next step, looked up ahead
+  bool l_ok = false;                                              // (not looked at before it is needed)
   auto look_up = [&]() {   // goes on to the next piece where this one has no step left
     while (l_next >= l_end) {
       Piece p;
@@ -460,22 +459,22 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       l_end = p.tok1;
       l_next = p.tok0 + warp * S::kStep;   // a piece may have no step for this warp
     }
-    l_row = -1;
     l_ok = lane < S::kStep && lane < l_end - l_next;
-    if (l_ok) l_row = token_row(a.c, l_seq, l_next + lane);
+    if (l_ok) l_page = __ldg(a.c.tables + l_seq * a.c.table_stride + page_of(a.c, l_next + lane));
   };
   // Requests the next step's rows; bit r of the result is set where row r is
   // a token to attend to.
   auto issue = [&]() -> uint32_t {
     if (l_next == INT_MAX) return 0;
-    if (l_ok && l_row < 0) raise_error(a.c.error, kErrIndex);
-    const uint32_t valid = __ballot_sync(0xffffffffu, l_row >= 0);
-    if (kFused && l_next + lane == l_len - 1) l_row = -1;   // the new token comes from shared memory
+    int row = l_ok ? row_in(a.c, l_page, l_next + lane) : -1;
+    if (l_ok && row < 0) raise_error(a.c.error, kErrIndex);
+    const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0);
+    if (kFused && l_next + lane == l_len - 1) row = -1;   // the new token comes from shared memory
     const uint32_t dst0 = ring_u + l_stage * (2 * S::kHalf);
 #pragma unroll
     for (int r0 = 0; r0 < S::kStep; r0 += kPerPass) {
       const int r = r0 + lane / S::kChunks;
-      const int from = __shfl_sync(0xffffffffu, l_row, r);
+      const int from = __shfl_sync(0xffffffffu, row, r);
       const T* src = src0 + max(from, 0) * row_size;
       const uint32_t dst = dst0 + r * (D * 2) + ((chunk ^ (r & 7)) << 4);
       cp_async16(dst, src, from >= 0);
@@ -487,6 +486,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     return valid;
   };
   look_up();
+  Piece p;
+  bool more = next_piece(a, rank, work, p);
+  if (more) request(p);
   uint32_t valid[S::kStages];   // of the steps under way, the next one first
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) {
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       const int groups = (p.parts + kGroup - 1) / kGroup;
       __syncthreads();
       if (tid == 0) {
-        const bool ready = *a.ws_magic == kWorkspaceMagic;
+        const bool ready = magic == kWorkspaceMagic;
         if (!ready) raise_error(a.c.error, kErrWorkspace);
         s_last = ready && arrive_last(a.counters + part_slot(a, p.r0, g0, unit), of);
       }
