@@ -489,10 +489,12 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   Piece p;
   bool more = next_piece(a, rank, work, p);
   if (more) request(p);
-  uint32_t valid[S::kStages];   // of the steps under way, the next one first
-#pragma unroll
+  uint32_t valid[S::kStages] = {};   // of the steps under way, the next one first
+#pragma unroll 1   // one copy of issue()
   for (int i = 0; i < S::kStages - 1; ++i) {
-    valid[i] = issue();
+#pragma unroll
+    for (int k = 0; k < S::kStages - 2; ++k) valid[k] = valid[k + 1];
+    valid[S::kStages - 2] = issue();
     cp_async_commit();
   }
 
