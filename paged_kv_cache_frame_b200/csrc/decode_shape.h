@@ -40,10 +40,10 @@ inline int decode_ranks(int units, int rows, bool fused, int warps, int num_sms)
 constexpr int decode_step(int D) { return D == 64 ? 32 : 16; }
 
 // Tiles that are not worth a join, while parts of them leave CTAs idle
-// (measured with tiles of four warps, 32 KB: 1, 2, 3 and 4 give 6.8, 7.4, 6.0,
-// 6.0 us for 16 heads of 300 tokens; 9.2, 9.6, 10.3, 10.9 for a step of two
-// sequences of up to 1000, 8 x 2 heads; 16.4, 15.4, 14.7, 13.4 for 8 x 8 heads
-// of 4096).
+// (with tiles of eight warps, 64 KB, 1, 2, 3 and 4 measured: 7.3, 5.3, 5.3, 5.3
+// us for 16 heads of 300 tokens; 9.4, 10.2, 11.1, 12.0 for a step of two
+// sequences of up to 1000, 8 x 2 heads; 12.3, 11.8, 12.1, 11.6 for 8 x 8 heads
+// of 4096; with tiles of four, 32 KB: 16.4, 15.4, 14.7, 13.4 for the last).
 constexpr int decode_part_tiles(int warps) { return warps == 8 ? 2 : 3; }
 
 // A sequence's own cost in tiles, in the line that the ranks share (1, 2, 3
