@@ -526,9 +526,9 @@ int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int
 size_t kv_decode_workspace_bytes(const kv_tokens* c, int q_heads);
 
 /* kv_decode_workspace_init -- prepare a workspace (16-byte aligned, of at
- * least kv_decode_workspace_bytes) for the calls of one batch and number of
- * query heads; two memsets on `stream`. Calls leave it prepared and keep no
- * result in it. Calls that may overlap on the GPU, captured ones among them,
+ * least kv_decode_workspace_bytes); two memsets on `stream`. It serves every
+ * batch and number of query heads on the device whose bytes it covers. Calls
+ * leave it prepared and keep no result in it. Calls that may overlap on the GPU, captured ones among them,
  * need a workspace each.
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY, KV_ERR_CUDA. */
 int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, size_t workspace_bytes, void* stream);
@@ -543,7 +543,8 @@ int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, s
  * inputs give equal bits. What the pool holds outside of the tokens seen does
  * not count; an infinity or NaN among them makes its outputs not finite. workspace: of kv_decode_workspace_init; one that was
  * not prepared raises the error word, and sequences split over several CTAs
- * are then not written. tables and lens must not change while a call runs.
+ * are then not written. tables and lens must not change while a call runs
+ * (outputs are then undefined, and the workspace needs preparing again).
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY (workspace),
  * KV_ERR_CUDA. */
 int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, int window, void* out, void* workspace,

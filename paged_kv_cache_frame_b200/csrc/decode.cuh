@@ -111,7 +111,7 @@ __device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, int len) {
   return ((uint32_t)(len - first_seen(a, len)) + (1u << a.tile_shift) - 1) >> a.tile_shift;
 }
 
-// Shared memory behind the rings. A unit's queries (as they come, and
+// Shared memory behind the rings. A piece's queries (as they come, and
 // rotated) take the place of the warps' O: never at once.
 template <int D, int NT, bool kFused, int W>
 struct Smem {
@@ -296,17 +296,17 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int of) {
 
 // Joins parts p0, p0 + step, ... (n of at most 32) of the sequence begun by
 // rank r0: O = sum_i 2^(m_i - M) O_i, l = sum_i 2^(m_i - M) l_i. The last round
-// writes O / l to `out` (the unit's first query row of the sequence), others the part in the
-// first one's place. A warp takes a query head at a time (of fewer heads
-// than warps, if they divide these, several warps some of its parts each, added
-// up in `sums`), a lane a
-// part's weight, then all lanes the parts' rows with kPre of them in flight,
-// the first before the weights are known. All threads of the CTA.
+// writes O / l to `out` (the unit's first query row of the sequence), others
+// the part in the first one's place. A warp takes a query head at a time (of
+// fewer heads than warps, if they divide these, several warps some of its
+// parts each, added up in `sums`): a lane a part's weight, then all lanes the
+// parts' rows with kPre of them in flight, the first before the weights are
+// known. All threads of the CTA.
 template <int D, typename T, int kRows, int W>
 __device__ __forceinline__ void join_parts(const DecodeArgs& a, float* sums, int r0, uint32_t unit, int p0, int step, int n,
                                            int heads, T* out) {
   constexpr int V = D / 32;    // values of a lane
-  constexpr int kPre = 8;
+  constexpr int kPre = D == 128 ? 4 : 8;   // 16 registers: more and three CTAs' share is spilled (short batches +15%)
   using P = Pack<float, V>;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int share = W % heads == 0 ? W / heads : 1;                      // warps of a head
@@ -381,7 +381,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   constexpr int kRows = M::kRows;
   constexpr bool kFP16 = kIsFp16<T>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ bool s_last;
+  __shared__ bool s_last, s_more;
+  __shared__ Piece s_piece[2];   // this one and the next
+  __shared__ Split s_work;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t rank = blockIdx.x / a.units, unit = blockIdx.x - rank * a.units;
   const int h = unit / a.head_groups;                                   // its K/V head
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
 
   uint32_t magic = 0;
   if (tid == 0) magic = __ldcg(a.ws_magic);
-  Split work = split(a, rank);
+  Split ahead = split(a, rank);
   T* out = static_cast<T*>(a.out);
   const int q_heads = a.c.H * a.group;
   for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x) {
@@ -402,8 +404,6 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     if (seq_len(a.c, s) == 0)   // nothing to see
       for (int i = tid; i < q_heads * D; i += kThreads) out[(long long)s * q_heads * D + i] = from_f32<T>(0.f);
   }
-  if (work.t >= work.end) return;
-
   uint8_t* ring = smem + warp * (S::kStages * 2 * S::kHalf);
   const uint32_t ring_u = smem_u32(ring);
   const T* pool = static_cast<const T*>(a.c.pool);
@@ -435,7 +435,26 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     }
   };
 
-  Split ahead = work;
+  // The CTA's pieces, one after the other, as its last warp finds them: what
+  // the barriers below depend on is the same for all warps even if the lengths
+  // change under the launch, which must not be but must not hang.
+  if (tid == kThreads - 32) s_work = ahead;
+  int which = 0;   // of s_piece
+  auto find_next = [&](int to) {
+    if (warp == W - 1) {
+      __syncwarp();
+      Split work = s_work;
+      Piece next;
+      const bool found = next_piece(a, rank, work, next);
+      __syncwarp();
+      if (lane == 0) {
+        s_work = work;
+        s_more = found;
+        if (found) s_piece[to] = next;
+      }
+    }
+  };
+  find_next(0);
 
   // The loads' side runs kStages - 1 steps ahead of the products', over the
   // ends of units. Step i of a warp in a piece: tokens
@@ -486,9 +505,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     return valid;
   };
   look_up();
-  Piece p;
-  bool more = next_piece(a, rank, work, p);
-  if (more) request(p);
+  __syncthreads();
+  if (!s_more) return;
+  request(s_piece[0]);
   uint32_t valid[S::kStages] = {};   // of the steps under way, the next one first
 #pragma unroll 1   // one copy of issue()
   for (int i = 0; i < S::kStages - 1; ++i) {
@@ -504,12 +523,12 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   const uint64_t turn = on ? a.rope.turn[tid % (D / 2)] : 0;
 
   int stage = 0;
-  while (more) {
+  for (;;) {
+    const Piece& p = s_piece[which];
     const int tok0 = p.tok0 + warp * S::kStep, tok1 = p.tok1;
     const bool has_new = kFused && tok1 == p.len;   // the new token's row lies in this piece
-    Piece next;
 
-    __syncthreads();   // the last piece's results have been read
+    __syncthreads();   // the last piece's results, and where this one lies, have been read
     uint4* sq = reinterpret_cast<uint4*>(smem + M::kOffO);
     float* sf = reinterpret_cast<float*>(smem + M::kOffTurned);
     T* sn = reinterpret_cast<T*>(smem + M::kOffNew);
@@ -519,8 +538,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     const int row_of_new = row_in(a.c, new_page, p.len - 1);
     const int pos = a.positions ? new_pos : p.len - 1;
     if (has_new && tid < 2 * S::kChunks) reinterpret_cast<uint4*>(sn)[tid] = raw_new;
-    more = next_piece(a, rank, work, next);
-    if (more) request(next);
+    find_next(which ^ 1);
     if (kFused) {
       float c = 1.f, s = 0.f;
       if (on) rope_angle(turn, pos, a.rope.amplitude, c, s);
@@ -540,6 +558,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       }
     }
     __syncthreads();
+    if (s_more) request(s_piece[which ^ 1]);
     if (has_new && tid < 2 * S::kChunks) {
       if (row_of_new < 0) {
         if (tid == 0) raise_error(a.c.error, kErrIndex);
@@ -818,7 +837,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
         if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, 0, kGroup, groups, heads, to);
       }
     }
-    p = next;
+    if (!s_more) break;
+    which ^= 1;
   }
   cp_async_wait<0>();
 }

@@ -36,6 +36,9 @@ inline int decode_ranks(int units, int rows, bool fused, int warps, int num_sms)
   return n > 1 ? n : 1;
 }
 
+// CTAs of any launch whose units have more than one.
+inline int decode_most_ctas(int num_sms) { return 3 * num_sms; }
+
 // Tokens that a warp takes at a time (8 KB of K and V).
 constexpr int decode_step(int D) { return D == 64 ? 32 : 16; }
 

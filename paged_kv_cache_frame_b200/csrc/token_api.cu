@@ -109,7 +109,7 @@ DecodeLayout decode_layout(const kv_tokens* c, int q_heads) {
     const int ranks = pkv::decode_ranks(l.units, l.rows, shape & 1, shape & 2 ? 8 : 4, l.sms);
     if (ranks > 1 && (size_t)ranks * l.units > ctas) ctas = (size_t)ranks * l.units;
   }
-  l.counters = 4 * ctas * sizeof(uint32_t);
+  l.counters = 4 * (size_t)pkv::decode_most_ctas(l.sms) * sizeof(uint32_t);   // in one place whatever the heads
   l.off_counters = 256;
   l.off_ml = align256(l.off_counters + l.counters);
   l.off_o = align256(l.off_ml + 2 * ctas * l.rows * 8);

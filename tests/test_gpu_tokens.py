@@ -672,6 +672,19 @@ def test_unprepared_workspace_is_reported(pkv):
     b.cache.check_device()
 
 
+def test_one_workspace_for_all_heads(pkv):
+    """A workspace of the largest call serves batches of other heads and lengths in turn."""
+    batches = [Batch(pkv, [20000, 300], hkv, 64, 64, seed=29 + hkv) for hkv in (1, 3, 8)]
+    calls = [(b, randn((2, b.hkv * g, 64), b.dtype, b.g)) for b in batches for g in (1, 5, 16)]
+    most = max((b.cache.workspace_bytes(q.shape[1]), i) for i, (b, q) in enumerate(calls))[1]
+    ws = calls[most][0].cache.workspace(calls[most][1].shape[1])
+    for _ in range(2):
+        for b, q in calls:
+            assert torch.equal(b.cache.decode(q, workspace=ws), b.cache.decode(q))
+    b, q = calls[0]
+    assert_attended(b.cache.decode(q, workspace=ws), b, q)
+
+
 @pytest.mark.parametrize("seqs,hkv,g,n", [(1, 1, 1, 70000), (1, 1, 16, 40000), (2, 1, 5, 30000), (5, 1, 3, 9000), (1, 3, 2, 20011)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_many_parts(pkv, seqs, hkv, g, n, d):
