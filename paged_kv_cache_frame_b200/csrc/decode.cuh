@@ -44,15 +44,15 @@
 // every step). P is fed as a sum of two 16-bit values, its rounding and the
 // rest: rounding P alone would add an error as large as the output's own.
 // Groups of 9 to 16 take two blocks of heads in a pass (32 x 4 x 16 heads of
-// 128: 63 us, as two units 71).
+// 128: 62 us, as two units 71).
 //
 // Measured, inputs not in cache, of a copy's 6.54 TB/s:
 //   4 x 16 heads of 64, 77928 tokens, pages of 999     186 us  105%
-//   64 sequences of up to 8192, 8 x 4 heads of 128     148 us   99%
+//   64 sequences of up to 8192, 8 x 4 heads of 128     146 us  100%
 //   1 sequence of 262111, 4 x 8 heads of 128           88.6 us  93%
 //   1 sequence of 20352, 16 heads of 64                20.2 us  63%
-//   a step of 128 sequences, window 1500, 4 x 7 of 64  38.7 us  63%
-//   16 heads of 300 tokens                              5.3 us
+//   a step of 128 sequences, window 1500, 4 x 7 of 64  37.1 us  66%
+//   16 heads of 300 tokens                              5.6 us
 // The DRAM traffic is the algorithm's bytes. What is left in the shorter ones
 // is the start (lengths, then pages, then rows: 2 to 3 us), the join (2 to 3
 // us) and CTAs that end at different times.
