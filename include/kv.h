@@ -440,7 +440,8 @@ int kv_run_static(kv_cache_t* const* caches, int n_streams, int block, int tiles
  * All calls: device pointers belong to the caller and lie on the current
  * device, to which `stream` belongs. Calls do not synchronise and can be
  * captured. Inputs must not overlap outputs except where a call says so.
- * Sizes of zero are allowed and launch nothing.
+ * Sizes of zero are allowed and launch nothing; n_tokens and n_heads go up to
+ * 2^30.
  */
 
 /* kv_rotate also takes 32-bit tensors. */
@@ -555,7 +556,8 @@ int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, in
  * the launches and passes between them. k, v [n_seqs, H, D]; positions
  * [n_seqs] or NULL (lens[s] - 1). The new key counts in the pool's dtype, as
  * later steps read it; the rotated query is not rounded. A page that the
- * sequence's new token is written to must not be another sequence's as well.
+ * sequence's new token is written to must not be another sequence's as well,
+ * nor stand twice in its own row of the table.
  * Errors: as kv_decode. */
 int kv_decode_append(const kv_tokens* c, const kv_rows* k, const kv_rows* v, const kv_rows* q, int q_heads,
                      const kv_rope_t* rope, const int32_t* positions, float scale, int window, void* out,

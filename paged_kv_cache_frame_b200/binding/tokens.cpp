@@ -98,6 +98,7 @@ at::Tensor rotate(const c10::intrusive_ptr<Rope>& rope, const at::Tensor& x, con
   TORCH_CHECK_VALUE(x.dim() == 3, "x: shape ", shown(x.sizes()), ", expected [tokens, heads, head_dim]");
   check_device(x, "x");
   check_tensor(x, "x", x.sizes(), x.scalar_type(), x.device(), false);
+  TORCH_CHECK_VALUE(x.size(0) <= INT32_MAX && x.size(1) <= INT32_MAX && x.size(2) <= INT32_MAX, "x: too large");
   check_tensor(positions, "positions", {x.size(0)}, at::kInt, x.device(), true);
   if (given) check_tensor(*given, "out", x.sizes(), x.scalar_type(), x.device(), false);
   const c10::cuda::OptionalCUDAGuard guard(x.device());
@@ -193,7 +194,8 @@ at::Tensor decode(Tokens& t, const c10::optional<at::Tensor>& k, const c10::opti
   TORCH_CHECK_VALUE(heads >= 1 && heads % t.c.num_heads == 0, "q: ", heads, " heads, expected a multiple of the pool's ",
                     t.c.num_heads);
   if (given) check_tensor(*given, "out", shape, t.dtype, t.device, true);
-  TORCH_CHECK_VALUE(!scale || *scale != 0, "scale: 0 would weigh all tokens alike");
+  const float s = scale ? (float)*scale : 0.f;
+  TORCH_CHECK_VALUE(!scale || s != 0, "scale: 0 would weigh all tokens alike");
   TORCH_CHECK_VALUE(window >= INT32_MIN && window <= INT32_MAX, "window: out of range");
   if (workspace)
     TORCH_CHECK_VALUE(workspace->device() == t.device && workspace->is_contiguous(),
@@ -212,7 +214,6 @@ at::Tensor decode(Tokens& t, const c10::optional<at::Tensor>& k, const c10::opti
     ws = kept;
   }
   const kv_rows qr = rows_of(q);
-  const float s = scale ? (float)*scale : 0.f;
   if (k) {
     const kv_rows kr = rows_of(*k), vr = rows_of(*v);
     check_status(kv_decode_append(&t.c, &kr, &vr, &qr, (int)heads, rope ? rope->handle : nullptr, pos, s, (int)window,

@@ -88,6 +88,10 @@ int view_rope(const kv_rope_t* r, int head_dim, const std::string& who, pkv::Rop
   return KV_OK;
 }
 
+// Tokens and heads of a call: the kernels' row counters run a block's rows
+// past the last one in 31 bits.
+constexpr int kMaxCount = 1 << 30;
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // [magic | arrival counters | the parts' maxima and sums | their outputs], for
@@ -132,7 +136,9 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   int rc = view_cache(c, who, &a.c);
   if (rc != KV_OK) return rc;
   if ((rc = check_group(c, q_heads, who)) != KV_OK) return rc;
-  if (!std::isfinite(scale)) return api_fail(KV_ERR_ARG, who + ": scale is not finite");
+  const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
+  const float scale_log2 = (float)(s * 1.4426950408889634);   // the logits' own, in powers of two
+  if (!std::isfinite(scale_log2)) return api_fail(KV_ERR_ARG, who + ": scale is not finite, or too large");
   if (window < 0) return api_fail(KV_ERR_ARG, who + ": window < 0");
   if ((rc = view_rope(rope, c->head_dim, who, &a.rope)) != KV_OK) return rc;
   if (!aligned(positions, 4)) return api_fail(KV_ERR_ARG, who + ": positions not 4-byte aligned");
@@ -159,8 +165,7 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   a.ranks = pkv::decode_ranks(l.units, l.rows, fused, a.warps, l.sms);
   a.tile_shift = pkv::decode_tile_shift(c->head_dim, a.warps, c->n_seqs, (long long)c->table_width * c->page_size);
   a.part_tiles = pkv::decode_part_tiles(a.warps);
-  const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
-  a.scale_log2 = (float)(s * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   const cudaError_t e = c->head_dim == 64 ? pkv::launch_decode_d64(a, c->dtype, fused, (cudaStream_t)stream)
                                           : pkv::launch_decode_d128(a, c->dtype, fused, (cudaStream_t)stream);
   return e == cudaSuccess ? KV_OK : api_cuda_fail(e, (who + ": launch").c_str());
@@ -223,7 +228,8 @@ int kv_rotate(const kv_rope_t* rope, const kv_rows* x, const kv_rows* out, const
     const std::string who("kv_rotate");
     if (!rope) return api_fail(KV_ERR_ARG, who + ": NULL rope");
     if (dtype != KV_BF16 && dtype != KV_FP16 && dtype != KV_FP32) return api_fail(KV_ERR_UNSUPPORTED, who + ": unknown dtype");
-    if (n_tokens < 0 || n_heads < 0) return api_fail(KV_ERR_ARG, who + ": negative size");
+    if (n_tokens < 0 || n_heads < 0 || n_tokens > kMaxCount || n_heads > kMaxCount)
+      return api_fail(KV_ERR_ARG, who + ": n_tokens or n_heads out of range");
     if (head_dim < 2 || head_dim > KV_MAX_ROTATE_DIM || head_dim % 2 != 0)
       return api_fail(KV_ERR_ARG, who + ": head_dim must be even, 2..512");
     pkv::RotateArgs a;
@@ -259,7 +265,7 @@ int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int
     std::memset(&a, 0, sizeof(a));
     int rc = view_cache(c, who, &a.c);
     if (rc != KV_OK) return rc;
-    if (n_tokens < 0) return api_fail(KV_ERR_ARG, who + ": n_tokens < 0");
+    if (n_tokens < 0 || n_tokens > kMaxCount) return api_fail(KV_ERR_ARG, who + ": n_tokens out of range");
     if (!cu_new && n_tokens != c->n_seqs)
       return api_fail(KV_ERR_ARG, who + ": without cu_new there is one token per sequence");
     if (!aligned(cu_new, 4) || !aligned(positions, 4)) return api_fail(KV_ERR_ARG, who + ": cu_new or positions not 4-byte aligned");

@@ -799,6 +799,13 @@ def test_refused_calls(pkv):
     assert_attended(b.cache.decode(q), b, q)
 
 
+def test_a_scale_below_32_bits_is_refused(pkv):
+    b = Batch(pkv, [10], 2, 64, 16, seed=22)
+    for scale in (1e-60, -1e-60):
+        with pytest.raises(ValueError):   # 0 would stand for the default
+            b.cache.decode(randn((1, 2, 64), b.dtype, b.g), scale=scale)
+
+
 # ---------------------------------------------------------------- over a frame plan's pages
 @pytest.mark.parametrize("ps,d,dtype,frames", [(16, 64, "bf16", 12), (130, 128, "fp16", 7)])
 def test_decode_over_a_frame_plan(pkv, ps, d, dtype, frames):

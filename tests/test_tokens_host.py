@@ -223,6 +223,17 @@ def test_tensors_are_checked_before_the_call(pkv):
         pkv.PagedTokens(torch.zeros(4, 2, 16, 2, 64), None, None)
 
 
+def test_counts_and_scales_at_the_edge_of_their_types(pkv):
+    """Counts whose next row would not fit 31 bits, and scales that are finite but not in powers of two."""
+    r, x, c, big = pkv.Rope(2), rows(pkv), tokens(pkv), 1 << 30
+    for n, h in [(big + 1, 1), (2**31 - 1, 1), (1, big + 1), (1, 2**31 - 1)]:
+        assert code(pkv, pkv.kv_rotate, r.handle, x, x, 4096, n, h, 2, 0) == "ARG"
+    assert code(pkv, pkv.kv_append_tokens, c, x, x, 2**31 - 1, 4096) == "ARG"
+    for scale in (3e38, -3e38):
+        assert code(pkv, pkv.kv_decode, c, x, 2, scale, 0, 4096, 4096, big) == "ARG"
+        assert code(pkv, pkv.kv_decode_append, c, x, x, x, 2, None, None, scale, 0, 4096, 4096, big) == "ARG"
+
+
 # ---------------------------------------------------------------- index arithmetic
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_page_divisor(tmp_path):
