@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -53,6 +54,7 @@ void check_tensor(const at::Tensor& x, const char* name, at::IntArrayRef shape, 
   TORCH_CHECK_VALUE(x.sizes() == shape, name, ": shape ", shown(x.sizes()), ", expected ", shown(shape));
   TORCH_CHECK_VALUE(x.scalar_type() == dtype, name, ": dtype ", x.scalar_type(), ", expected ", dtype);
   TORCH_CHECK_VALUE(x.device() == device, name, ": on ", x.device(), ", expected ", device);
+  TORCH_CHECK_VALUE(!x.is_neg(), name, ": its values are not the memory's (resolve_neg() first)");
   if (x.is_contiguous()) return;
   TORCH_CHECK_VALUE(!contiguous, name, ": must be contiguous");
   TORCH_CHECK_VALUE(x.stride(-1) == 1 || x.size(-1) <= 1 || x.numel() == 0, name, ": the last dimension must be contiguous");
@@ -66,6 +68,16 @@ void check_device(const at::Tensor& x, const char* name) {
 void check_no_gradient(const at::Tensor& x, const char* name) {
   TORCH_CHECK_VALUE(!x.requires_grad() || !at::GradMode::is_enabled(), name,
                     ": requires a gradient, which this operator does not have (detach it or call under torch.no_grad)");
+}
+
+// A tensor that a call writes: apart from its own elements, and counted as
+// changed, so that autograd notices where it was saved.
+void check_written(const at::Tensor& x, const char* name) {
+  check_no_gradient(x, name);
+  TORCH_CHECK_VALUE(at::has_internal_overlap(x) != at::MemOverlap::Yes, name, ": its elements share memory (an expanded tensor)");
+}
+void written(const at::Tensor& x) {
+  if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
 }
 
 // A [n, heads, head_dim] tensor's rows; the stride of a dimension of one
@@ -100,13 +112,17 @@ at::Tensor rotate(const c10::intrusive_ptr<Rope>& rope, const at::Tensor& x, con
   check_tensor(x, "x", x.sizes(), x.scalar_type(), x.device(), false);
   TORCH_CHECK_VALUE(x.size(0) <= INT32_MAX && x.size(1) <= INT32_MAX && x.size(2) <= INT32_MAX, "x: too large");
   check_tensor(positions, "positions", {x.size(0)}, at::kInt, x.device(), true);
-  if (given) check_tensor(*given, "out", x.sizes(), x.scalar_type(), x.device(), false);
+  if (given) {
+    check_tensor(*given, "out", x.sizes(), x.scalar_type(), x.device(), false);
+    check_written(*given, "out");
+  }
   const c10::cuda::OptionalCUDAGuard guard(x.device());
   at::Tensor out = given ? *given : empty_rows(x);
   const kv_rows from = rows_of(x), to = rows_of(out);
   check_status(kv_rotate(rope->handle, &from, &to, positions.data_ptr<int32_t>(), (int)x.size(0), (int)x.size(1),
                          (int)x.size(2), code, inverse, c10::cuda::getCurrentCUDAStream(x.device().index()).stream()),
                "kv_rotate");
+  if (given) written(out);
   return out;
 }
 
@@ -172,6 +188,7 @@ void append(Tokens& t, const at::Tensor& k, const at::Tensor& v, const c10::opti
             const c10::optional<at::Tensor>& positions) {
   const int64_t n = cu_new && k.dim() == 3 ? k.size(0) : t.c.n_seqs;
   check_new(t, k, v, n);
+  check_written(t.pool, "pool");
   TORCH_CHECK_VALUE(n <= INT32_MAX, "k: too many tokens");
   const int32_t* cu = index_of(cu_new, "cu_new", (int64_t)t.c.n_seqs + 1, t.device);
   const int32_t* pos = index_of(positions, "positions", n, t.device);
@@ -179,6 +196,7 @@ void append(Tokens& t, const at::Tensor& k, const at::Tensor& v, const c10::opti
   const kv_rows kr = rows_of(k), vr = rows_of(v);
   check_status(kv_append_tokens(&t.c, &kr, &vr, (int)n, cu, rope ? rope->handle : nullptr, pos, stream_of(t)),
                "kv_append_tokens");
+  written(t.pool);
 }
 
 // decode, and decode_append where k and v are given.
@@ -187,13 +205,17 @@ at::Tensor decode(Tokens& t, const c10::optional<at::Tensor>& k, const c10::opti
                   const c10::optional<double>& scale, int64_t window, const c10::optional<at::Tensor>& workspace) {
   TORCH_CHECK_VALUE(q.dim() == 3, "q: shape ", shown(q.sizes()), ", expected [n_seqs, q heads, head_dim]");
   if (k) check_new(t, *k, *v, t.c.n_seqs);
+  check_no_gradient(t.pool, "pool");
   const int64_t heads = q.size(1);
   const int64_t shape[] = {t.c.n_seqs, heads, t.c.head_dim};
   check_tensor(q, "q", shape, t.dtype, t.device, false);
   check_no_gradient(q, "q");
   TORCH_CHECK_VALUE(heads >= 1 && heads % t.c.num_heads == 0, "q: ", heads, " heads, expected a multiple of the pool's ",
                     t.c.num_heads);
-  if (given) check_tensor(*given, "out", shape, t.dtype, t.device, true);
+  if (given) {
+    check_tensor(*given, "out", shape, t.dtype, t.device, true);
+    check_written(*given, "out");
+  }
   const float s = scale ? (float)*scale : 0.f;
   TORCH_CHECK_VALUE(!scale || s != 0, "scale: 0 would weigh all tokens alike");
   TORCH_CHECK_VALUE(window >= INT32_MIN && window <= INT32_MAX, "window: out of range");
@@ -219,10 +241,12 @@ at::Tensor decode(Tokens& t, const c10::optional<at::Tensor>& k, const c10::opti
     check_status(kv_decode_append(&t.c, &kr, &vr, &qr, (int)heads, rope ? rope->handle : nullptr, pos, s, (int)window,
                                   out.data_ptr(), ws.data_ptr(), ws.nbytes(), stream),
                  "kv_decode_append");
+    written(t.pool);
   } else {
     check_status(kv_decode(&t.c, &qr, (int)heads, s, (int)window, out.data_ptr(), ws.data_ptr(), ws.nbytes(), stream),
                  "kv_decode");
   }
+  if (given) written(out);
   return out;
 }
 
@@ -291,7 +315,9 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (handle), 
 PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (rope, x, positions, out, inverse)
   if (n != 5) return expect(n, 5);
   return guarded([&]() -> PyObject* {
-    const auto& rope = *rope_slot(a[0]);
+    const auto* slot = rope_slot(a[0]);
+    TORCH_CHECK_TYPE(slot, "rope: None");
+    const auto& rope = *slot;
     const at::Tensor& x = tensor(a[1], "x");
     const at::Tensor& positions = tensor(a[2], "positions");
     const auto out = optional_tensor(a[3], "out");

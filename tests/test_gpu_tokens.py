@@ -806,6 +806,44 @@ def test_a_scale_below_32_bits_is_refused(pkv):
             b.cache.decode(randn((1, 2, 64), b.dtype, b.g), scale=scale)
 
 
+def test_written_tensors_count_as_changed(pkv):
+    """What autograd saved and a call then wrote: its backward pass says so, as for torch's own in-place calls."""
+    b, rope = Batch(pkv, [10, 20], 2, 64, 16, seed=23), pkv.Rope(64)
+    k, q, pos = randn((2, 2, 64), b.dtype, b.g), randn((2, 4, 64), b.dtype, b.g), b.len_t - 1
+    x, out = randn((2, 2, 64), torch.float32, b.g), torch.empty_like(q)
+    for saved, call in [(x, lambda: rope.rotate(x, pos, out=x)), (b.pool, lambda: b.cache.append(k, k)),
+                        (b.pool, lambda: b.cache.decode_append(k, k, q)), (out, lambda: b.cache.decode(q, out=out))]:
+        w = torch.ones((), device="cuda", dtype=saved.dtype, requires_grad=True)
+        y = (saved * w).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    version = b.pool._version
+    b.cache.decode(q)
+    assert b.pool._version == version
+    with torch.inference_mode():   # its tensors have no versions
+        z = x * 1
+        rope.rotate(z, pos, out=z)
+        b.cache.decode(q * 1, out=q * 1)
+
+
+def test_tensors_that_stand_for_others_are_refused(pkv):
+    b, rope = Batch(pkv, [10, 20], 2, 64, 16, seed=24), pkv.Rope(64)
+    k, q, pos = randn((2, 2, 64), b.dtype, b.g), randn((2, 4, 64), b.dtype, b.g), b.len_t - 1
+    wide = torch.empty((2, 1, 64), device="cuda").expand(2, 3, 64)
+    for call in (lambda: rope.rotate(wide, pos, out=wide), lambda: rope.rotate(torch.empty(2, 3, 64, device="cuda"), pos, out=wide),
+                 lambda: rope.rotate(torch._neg_view(wide.contiguous()), pos), lambda: b.cache.decode(torch._neg_view(q)),
+                 lambda: b.cache.append(k, torch._neg_view(k)), lambda: b.cache.decode(q, out=torch.empty_like(q).requires_grad_())):
+        with pytest.raises(ValueError):
+            call()
+    b.pool.requires_grad_()
+    for call in (lambda: b.cache.decode(q), lambda: b.cache.append(k, k), lambda: b.cache.decode_append(k, k, q)):
+        with pytest.raises(ValueError):
+            call()
+    with torch.no_grad():
+        assert_attended(b.cache.decode(q), b, q)
+
+
 # ---------------------------------------------------------------- over a frame plan's pages
 @pytest.mark.parametrize("ps,d,dtype,frames", [(16, 64, "bf16", 12), (130, 128, "fp16", 7)])
 def test_decode_over_a_frame_plan(pkv, ps, d, dtype, frames):
