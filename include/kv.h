@@ -555,7 +555,9 @@ int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, in
  * sequence, the rotation of q at the same position, and kv_decode, without
  * the launches and passes between them. k, v [n_seqs, H, D]; positions
  * [n_seqs] or NULL (lens[s] - 1). The new key counts in the pool's dtype, as
- * later steps read it; the rotated query is not rounded. A page that the
+ * later steps read it; the rotated query is not rounded. A length past the
+ * table's end has no slot for its new token: nothing of it is written, and the
+ * tokens that the table names are attended to as they stand. A page that the
  * sequence's new token is written to must not be another sequence's as well,
  * nor stand twice in its own row of the table.
  * Errors: as kv_decode. */

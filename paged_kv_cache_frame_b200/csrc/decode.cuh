@@ -164,8 +164,8 @@ struct Split {
   // Where place t lies: place `at` of the sequence's `size`.
   int seq;
   uint32_t at, size, tiles;
-  int len, later;     // the lengths of seq and seq + 1: read a sequence ahead, as a load takes
-                      // about a microsecond while the memory is busy
+  int raw, later;     // the lengths of seq and seq + 1 as they stand: read a sequence ahead, as a load
+                      // takes about a microsecond while the memory is busy
 
   __device__ __forceinline__ uint32_t rank_of(uint32_t place) const {
     const uint32_t lower = more * (each + 1);
@@ -175,7 +175,7 @@ struct Split {
 
 // The tokens of one sequence that the CTA takes.
 struct Piece {
-  int seq, len;       // and the sequence's length
+  int seq, raw;       // and the sequence's length as it stands: past the table's end there is no new token
   int tok0, tok1;     // tokens [tok0, tok1)
   int r0, parts;      // the sequence's first rank, and in how many it lies
 };
@@ -190,9 +190,9 @@ __device__ __forceinline__ uint32_t parts_of(const DecodeArgs& a, uint32_t tiles
 // On to the next sequence's places.
 __device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
   ++l.seq;
-  l.len = held(a.c, l.later);
+  l.raw = l.later;
   l.later = raw_len(a, l.seq + 1);
-  l.tiles = tiles_of(a, l.len);
+  l.tiles = tiles_of(a, held(a.c, l.raw));
   l.size = l.by_parts ? parts_of(a, l.tiles) : l.tiles ? l.tiles + kSeqCost : 0;
   l.at = 0;
 }
@@ -221,10 +221,10 @@ __device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t rank, S
     }
     if (tile0 == tile1) continue;
     p.seq = l.seq;
-    p.len = l.len;
-    const int seen = first_seen(a, l.len);
+    p.raw = l.raw;
+    const int len = held(a.c, l.raw), seen = first_seen(a, len);
     p.tok0 = seen + (int)(tile0 << a.tile_shift);
-    p.tok1 = tile1 == l.tiles ? p.len : seen + (int)(tile1 << a.tile_shift);
+    p.tok1 = tile1 == l.tiles ? len : seen + (int)(tile1 << a.tile_shift);
     return true;
   }
   return false;
@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     }
     if (kFused) {
       if (a.positions) new_pos = __ldg(a.positions + p.seq);
-      if (p.tok1 == p.len) {
-        new_page = __ldg(a.c.tables + p.seq * a.c.table_stride + page_of(a.c, p.len - 1));
+      if (p.tok1 == p.raw) {
+        new_page = __ldg(a.c.tables + p.seq * a.c.table_stride + page_of(a.c, p.tok1 - 1));
         if (tid < 2 * S::kChunks) {
           const RowsIn& from = tid < S::kChunks ? a.k : a.v;
           raw_new = *reinterpret_cast<const uint4*>(static_cast<const T*>(from.p) + p.seq * from.token_stride +
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   const int chunk = lane % S::kChunks;
   const long long row_size = (long long)a.c.H * D;
   const T* const src0 = pool + h * D + chunk * 8;                 // the lane's chunk of the head in row 0
-  int l_seq = 0, l_len = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
+  int l_seq = 0, l_raw = 0, l_next = 0, l_end = 0, l_stage = 0;   // next token and end of this warp's steps
   int l_page = 0;                                                 // the lane's page of the next step, looked up ahead
   bool l_ok = false;                                              // (not looked at before it is needed)
   auto look_up = [&]() {   // goes on to the next piece where this one has no step left
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
         return;
       }
       l_seq = p.seq;
-      l_len = p.len;
+      l_raw = p.raw;
       l_end = p.tok1;
       l_next = p.tok0 + warp * S::kStep;   // a piece may have no step for this warp
     }
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     int row = l_ok ? row_in(a.c, l_page, l_next + lane) : -1;
     if (l_ok && row < 0) raise_error(a.c.error, kErrIndex);
     const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0);
-    if (kFused && l_next + lane == l_len - 1) row = -1;   // the new token comes from shared memory
+    if (kFused && l_next + lane == l_raw - 1) row = -1;   // the new token comes from shared memory
     const uint32_t dst0 = ring_u + l_stage * (2 * S::kHalf);
 #pragma unroll
     for (int r0 = 0; r0 < S::kStep; r0 += kPerPass) {
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
   for (;;) {
     const Piece& p = s_piece[which];
     const int tok0 = p.tok0 + warp * S::kStep, tok1 = p.tok1;
-    const bool has_new = kFused && tok1 == p.len;   // the new token's row lies in this piece
+    const bool has_new = kFused && tok1 == p.raw;   // the new token's row lies in this piece
 
     __syncthreads();   // the last piece's results, and where this one lies, have been read
     uint4* sq = reinterpret_cast<uint4*>(smem + M::kOffO);
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
 #pragma unroll
     for (int x = 0; x < kQ; ++x)
       if (x * kThreads + tid < kRows * S::kChunks) sq[x * kThreads + tid] = raw[x];
-    const int row_of_new = row_in(a.c, new_page, p.len - 1);
-    const int pos = a.positions ? new_pos : p.len - 1;
+    const int row_of_new = row_in(a.c, new_page, tok1 - 1);
+    const int pos = a.positions ? new_pos : held(a.c, p.raw) - 1;
     if (has_new && tid < 2 * S::kChunks) reinterpret_cast<uint4*>(sn)[tid] = raw_new;
     find_next(which ^ 1);
     if (kFused) {
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       for (int k = 0; k < S::kStages - 1; ++k) valid[k] = valid[k + 1];
       const uint32_t ks = ring_u + stage * (2 * S::kHalf), vs = ks + S::kHalf;
       if (kFused && has_new) {
-        const int r = p.len - 1 - (tok0 + i * S::kStride);
+        const int r = tok1 - 1 - (tok0 + i * S::kStride);
         if (r >= 0 && r < S::kStep) {
           if (lane < 2 * S::kChunks) {
             const int chunk = lane % S::kChunks;
