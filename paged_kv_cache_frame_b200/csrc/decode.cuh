@@ -43,6 +43,10 @@
 // bytes need (tcgen05 would add a trip of S and P through tensor memory to
 // every step). P is fed as a sum of two 16-bit values, its rounding and the
 // rest: rounding P alone would add an error as large as the output's own.
+// fp16 has few values far below 1, so there P counts from kLift powers of two
+// below the maximum: what is left of a weight is within 2^-38 of the largest
+// one (2^-25 without), which matters where one key takes nearly all of it and
+// its value is small.
 // Groups of 9 to 16 take two blocks of heads in a pass (32 x 4 x 16 heads of
 // 128: 62 us, as two units 71).
 //
@@ -69,7 +73,13 @@ namespace pkv {
 
 namespace {
 
-constexpr float kSlack = 8.f;   // growth of a score, in powers of two, that the running max lets pass
+// In powers of two: how far the reference that P counts from lies below the
+// scores' running maximum, and the growth of a score that it lets pass. P
+// stays below 2^(kLift + kSlack): 2^15 in fp16, which ends at 2^16.
+template <typename T>
+constexpr float kLift = kIsFp16<T> ? 13.f : 0.f;
+template <typename T>
+constexpr float kSlack = kIsFp16<T> ? 2.f : 8.f;
 constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
 constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
@@ -677,9 +687,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
             for (int e = 0; e < 4; ++e)
               if (!(seen >> (b * 16 + lane / 4 + (e >> 1) * 8) & 1)) sc[b][n][e] = -INFINITY;
       }
-      // The reference m follows the scores' maximum only when one exceeds it
-      // by kSlack (a power of two: p stays below 2^kSlack, and O and l have
-      // the same factor). Mostly a vote is all it takes.
+      // The reference m (kLift below the maximum) follows the scores only
+      // when one exceeds it by kSlack more; O and l have the same factor.
+      // Mostly a vote is all it takes.
       float top[NT][2];
       bool grew = false;
 #pragma unroll
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
         for (int c = 0; c < 2; ++c) {
           top[n][c] = fmaxf(sc[0][n][c], sc[0][n][c + 2]);
           if constexpr (S::kM == 2) top[n][c] = fmaxf(top[n][c], fmaxf(sc[1][n][c], sc[1][n][c + 2]));
-          grew |= top[n][c] > m[n][c] + kSlack;
+          grew |= top[n][c] > m[n][c] + (kLift<T> + kSlack<T>);
         }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -698,6 +708,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
             float x = top[n][c];
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            x -= kLift<T>;
             const float f = x > m[n][c] ? ex2_approx(m[n][c] - x) : 1.f;   // 0 from -inf
             m[n][c] = fmaxf(x, m[n][c]);
             l[n][c] *= f;

@@ -35,3 +35,45 @@ def test_a_step_past_the_table_writes_nothing(pkv, held, hkv, g, d, page, dtype,
         assert_appended(b, before, [1, 1, 1], k, v, None)
         b.lens = [held, 40, 0]
         assert_attended(out, b, q, window=window)
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,g,fused", [(64, 1, False), (128, 4, False), (64, 16, False), (128, 2, True)])
+def test_weights_far_below_the_largest(pkv, dtype, d, g, fused):
+    """A key that takes nearly all of the weight and whose value is zero: the output is what the others' weights leave.
+    Both the weights' sum and their products have to hold them: 2^-38 of the largest weight is the least that fp16 pools
+    resolve (decode.cuh), a term per token."""
+    gaps = [6, 8, 10, 11, 12, 13, 14, 15, 16]       # in units of e: the others' weights are e^-gap each
+    b = Batch(pkv, [2048 + 37 * i for i in range(len(gaps))], 8, d, 64, dtype, seed=32)
+    b.pool.zero_()
+    for s, gap in enumerate(gaps):
+        n = b.lens[s]
+        j = torch.arange(n, device="cuda")
+        p, r = b.where(s, j)
+        v = (64 + 32 * torch.rand((n, 8, d), generator=b.g, device="cuda")).to(b.dtype)
+        k = (randn((n, 8, d), b.dtype, b.g) * 2**-6).to(b.dtype)
+        sink = j % 512 == 3                         # in every warp's share
+        k[sink] = 0
+        k[sink, :, 0] = gap * math.sqrt(d) / 8
+        v[sink] = 0
+        b.pool[p, 0, r], b.pool[p, 1, r] = k, v
+    q = torch.zeros((len(gaps), 8 * g, d), dtype=b.dtype, device="cuda")
+    q[..., 0] = 8
+    q[..., 1:] = randn((len(gaps), 8 * g, d - 1), b.dtype, b.g) * 2**-4
+    if fused:
+        last = [b.where(s, torch.tensor([n - 1], device="cuda")) for s, n in enumerate(b.lens)]
+        new = [torch.cat([b.pool[p, x, r] for p, r in last]) for x in (0, 1)]
+        out = b.cache.decode_append(new[0], new[1], q)
+    else:
+        out = b.cache.decode(q)
+    b.cache.check_device()
+    eps, tiny = half_step(b.dtype)
+    for s, n in enumerate(b.lens):
+        k, v = b.kv(s, n)
+        want, w, flat, most, seen = attended(k, v, q[s].double(), d ** -0.5, 0)
+        assert float(want.abs().min()) > 0
+        rel = most * d * 2**-23 + 2**-16 + (seen / 16 + 64) * 2**-23
+        tol = eps * want.abs() + tiny + 2 * rel * w * (1 + eps) + flat * 2**-38
+        err = (out[s].double() - want).abs()
+        assert bool((err <= tol).all()), f"gap {gaps[s]}: worst {float((err / tol).max()):.1f} of what is allowed"
