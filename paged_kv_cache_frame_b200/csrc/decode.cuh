@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
 #pragma unroll
       for (int k = 0; k < S::kStages - 1; ++k) valid[k] = valid[k + 1];
       const uint32_t ks = ring_u + stage * (2 * S::kHalf), vs = ks + S::kHalf;
-      if (kFused && has_new) {
+      if (kFused && has_new && row_of_new >= 0) {   // a token without a page leaves its row zero
         const int r = tok1 - 1 - (tok0 + i * S::kStride);
         if (r >= 0 && r < S::kStep) {
           if (lane < 2 * S::kChunks) {

@@ -77,3 +77,23 @@ def test_weights_far_below_the_largest(pkv, dtype, d, g, fused):
         tol = eps * want.abs() + tiny + 2 * rel * w * (1 + eps) + flat * 2**-38
         err = (out[s].double() - want).abs()
         assert bool((err <= tol).all()), f"gap {gaps[s]}: worst {float((err / tol).max()):.1f} of what is allowed"
+
+
+# ---------------------------------------------------------------- infinities in masked places
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("d,g", [(64, 2), (128, 16)])
+def test_a_new_token_without_a_page_counts_for_nothing(pkv, bad, d, g):
+    """Its key and value, infinite ones too, reach no output."""
+    b = Batch(pkv, [17, 40, 5000], 2, d, 16, seed=33)
+    t = b.tables.clone()
+    t[0, 1] = -7
+    t[2, 4999 // 16] = b.pool.shape[0]
+    c = pkv.PagedTokens(b.pool, t, b.len_t)
+    q = randn((3, 2 * g, d), b.dtype, b.g)
+    k, v = randn((3, 2, d), b.dtype, b.g), randn((3, 2, d), b.dtype, b.g)
+    k[0], v[0], k[2], v[2] = bad, bad, bad, bad
+    out = c.decode_append(k, v, q)
+    with pytest.raises(pkv.KVError):
+        c.check_device()
+    b.lens = [16, 40, 4992]
+    assert_attended(out, b, q, extra=2**-16)
