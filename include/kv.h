@@ -542,9 +542,11 @@ int kv_decode_workspace_init(const kv_tokens* c, int q_heads, void* workspace, s
  * [n_seqs, q_heads, D] contiguous, in the pool's dtype. scale 0 is 1/sqrt(D).
  * Rows of length 0 give zeros. fp32 statistics and sums, rounded once; equal
  * inputs give equal bits. What the pool holds outside of the tokens seen does
- * not count; an infinity or NaN among them makes its outputs not finite. workspace: of kv_decode_workspace_init; one that was
- * not prepared raises the error word, and sequences split over several CTAs
- * are then not written. tables and lens must not change while a call runs
+ * not count. A key whose score is -inf has no weight; where all are, the
+ * outputs are NaN. Any other infinity or NaN among the tokens seen makes the
+ * outputs that it reaches not finite.
+ * workspace: of kv_decode_workspace_init; one that was not prepared raises the
+ * error word, and sequences split over several CTAs are then not written. tables and lens must not change while a call runs
  * (outputs are then undefined, and the workspace needs preparing again).
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CAPACITY (workspace),
  * KV_ERR_CUDA. */
@@ -559,7 +561,8 @@ int kv_decode(const kv_tokens* c, const kv_rows* q, int q_heads, float scale, in
  * table's end has no slot for its new token: nothing of it is written, and the
  * tokens that the table names are attended to as they stand. A page that the
  * sequence's new token is written to must not be another sequence's as well,
- * nor stand twice in its own row of the table.
+ * nor stand twice in its own row of the table. Infinite keys in the pool
+ * make outputs NaN here (of the query's two parts one may be zero).
  * Errors: as kv_decode. */
 int kv_decode_append(const kv_tokens* c, const kv_rows* k, const kv_rows* v, const kv_rows* q, int q_heads,
                      const kv_rope_t* rope, const int32_t* positions, float scale, int window, void* out,

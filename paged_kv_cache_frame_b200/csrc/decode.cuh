@@ -61,6 +61,7 @@
 // is the start (lengths, then pages, then rows: 2 to 3 us), the join (2 to 3
 // us) and CTAs that end at different times.
 #pragma once
+#include <float.h>
 #include <limits.h>
 
 #include "decode_shape.h"
@@ -80,6 +81,9 @@ template <typename T>
 constexpr float kLift = kIsFp16<T> ? 13.f : 0.f;
 template <typename T>
 constexpr float kSlack = kIsFp16<T> ? 2.f : 8.f;
+// The maximum of tokens whose scores are all -inf, where that of no token is
+// -inf: their sum is 0 as well, but their softmax has no value.
+constexpr float kLowest = -FLT_MAX;
 constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
 constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
@@ -293,6 +297,12 @@ __device__ __forceinline__ long long part_slot(const DecodeArgs& a, int r0, int 
   return 2LL * ((long long)(r0 + p) * a.units + unit) + (p == 0 ? 1 : 0);
 }
 
+// What an output is divided by, inverted: without a token seen (a sequence of
+// pages that are none) it is zero, with scores of -inf alone not a number.
+__device__ __forceinline__ float inverse_sum(float top, float sum) {
+  return sum > 0.f ? 1.f / sum : top == -INFINITY ? 0.f : NAN;
+}
+
 // Adds one to a counter; true for the arrival that completes `of`, with the
 // others' writes visible to it. Called by one thread, after a barrier behind
 // the CTA's writes.
@@ -365,7 +375,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, float* sums, int
         for (int e = 0; e < V; ++e) acc[e] += sums[((warp + k) * 32 + lane) * V + e];
     }
     if (out) {
-      const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
+      const float inv = inverse_sum(top, sum);
       uint32_t* to = reinterpret_cast<uint32_t*>(out + i * D + lane * V);
 #pragma unroll
       for (int e = 0; e < V; e += 2) to[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
@@ -616,6 +626,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
 
+    uint32_t any = 0;   // a token was seen
     const int n_steps = tok0 < tok1 ? (tok1 - tok0 + S::kStride - 1) / S::kStride : 0;
     for (int i = 0; i < n_steps; ++i) {
       cp_async_wait<S::kStages - 2>();
@@ -623,6 +634,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       valid[S::kStages - 1] = issue();
       cp_async_commit();
       const uint32_t seen = valid[0];
+      any |= seen;
 #pragma unroll
       for (int k = 0; k < S::kStages - 1; ++k) valid[k] = valid[k + 1];
       const uint32_t ks = ring_u + stage * (2 * S::kHalf), vs = ks + S::kHalf;
@@ -761,9 +773,11 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+        if (any && m[n][c] == -INFINITY) m[n][c] = kLowest;
+      }
 
     // Join the warps in shared memory, a block of heads at a time.
     float* wo = reinterpret_cast<float*>(smem + M::kOffO);
@@ -814,7 +828,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
           }
           const int row = first + i;
           if (whole) {
-            const float r = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // no page was valid: zeros
+            const float r = inverse_sum(top, sum);
             *reinterpret_cast<uint32_t*>(out + ((long long)p.seq * q_heads + q0 + row) * D + d) =
                 pack2<T>(a0 * r, a1 * r);
           } else {

@@ -97,3 +97,30 @@ def test_a_new_token_without_a_page_counts_for_nothing(pkv, bad, d, g):
         c.check_device()
     b.lens = [16, 40, 4992]
     assert_attended(out, b, q, extra=2**-16)
+
+
+@pytest.mark.parametrize("lens,hkv,g,d,dtype", [
+    ([1], 1, 1, 64, "bf16"), ([300, 7], 2, 3, 128, "fp16"), ([20000], 1, 16, 64, "fp16"), ([30000] * 3, 1, 1, 64, "bf16")])
+def test_scores_that_are_all_minus_infinity(pkv, lens, hkv, g, d, dtype):
+    """A softmax over nothing but -inf has no value; with a finite score among them the others have no weight. (Zeros are
+    for rows that see no token.)"""
+    b = Batch(pkv, lens, hkv, d, 64, dtype, seed=34)
+    q = randn((len(lens), hkv * g, d), b.dtype, b.g).abs() + 0.1
+    keep = b.pool.clone()
+    for s, n in enumerate(lens):
+        p, r = b.where(s, torch.arange(n, device="cuda"))
+        b.pool[p, 0, r] = -math.inf
+    assert bool(b.cache.decode(q).isnan().all())
+    some = [max(1, n // 3) for n in lens]            # the first third as it was
+    kv = []
+    for s, n in enumerate(some):
+        p, r = b.where(s, torch.arange(n, device="cuda"))
+        b.pool[p, 0, r] = keep[p, 0, r]
+        kv.append(b.kv(s, n))
+    out = b.cache.decode(q)
+    c = Batch.__new__(Batch)
+    c.lens, c.d = some, d
+    assert_attended(out, c, q, kv=kv)
+    b.len_t.zero_()
+    assert bool((b.cache.decode(q) == 0).all())
+    b.cache.check_device()
