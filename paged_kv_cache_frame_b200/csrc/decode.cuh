@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
       for (int i = tid / (D / 2); i < kRows; i += kThreads / (D / 2)) {
         float x = to_f32(raw_q[i * D + e0]), y = to_f32(raw_q[i * D + e1]);
         if (on) rope_turn(x, y, c, s);
+        if constexpr (kFP16) x *= a.q_down, y *= a.q_down;   // a power of two: into the range of the two values below
         sf[i * D + e0] = x;
         sf[i * D + e1] = y;
       }

@@ -137,10 +137,18 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   if (rc != KV_OK) return rc;
   if ((rc = check_group(c, q_heads, who)) != KV_OK) return rc;
   const double s = scale != 0 ? (double)scale : 1 / std::sqrt((double)c->head_dim);
-  const float scale_log2 = (float)(s * 1.4426950408889634);   // the logits' own, in powers of two
-  if (!std::isfinite(scale_log2)) return api_fail(KV_ERR_ARG, who + ": scale is not finite, or too large");
+  if (!std::isfinite((float)(s * 1.4426950408889634)))   // the logits' own, in powers of two
+    return api_fail(KV_ERR_ARG, who + ": scale is not finite, or too large");
   if (window < 0) return api_fail(KV_ERR_ARG, who + ": window < 0");
   if ((rc = view_rope(rope, c->head_dim, who, &a.rope)) != KV_OK) return rc;
+  // A rotated query may be amplitude * sqrt(2) times as large as its type's
+  // largest value. In fp16, which has no range to spare, the kernel takes it
+  // down by the power of two that covers that, and the scale up.
+  int down = 0;
+  if (c->dtype == KV_FP16 && a.rope.rot > 0) std::frexp(a.rope.amplitude * 1.4142135623730951, &down);
+  if (down < 0) down = 0;
+  const float scale_log2 = (float)std::ldexp(s * 1.4426950408889634, down);
+  if (!std::isfinite(scale_log2)) return api_fail(KV_ERR_ARG, who + ": scale is too large for the rotation's amplitude");
   if (!aligned(positions, 4)) return api_fail(KV_ERR_ARG, who + ": positions not 4-byte aligned");
   if (c->n_seqs == 0) return KV_OK;
   if ((rc = view_rows(q, "q", who, &a.q)) != KV_OK) return rc;
@@ -166,6 +174,7 @@ int decode_impl(const kv_tokens* c, const kv_rows* q, int q_heads, const kv_rows
   a.tile_shift = pkv::decode_tile_shift(c->head_dim, a.warps, c->n_seqs, (long long)c->table_width * c->page_size);
   a.part_tiles = pkv::decode_part_tiles(a.warps);
   a.scale_log2 = scale_log2;
+  a.q_down = (float)std::ldexp(1.0, -down);
   const cudaError_t e = c->head_dim == 64 ? pkv::launch_decode_d64(a, c->dtype, fused, (cudaStream_t)stream)
                                           : pkv::launch_decode_d128(a, c->dtype, fused, (cudaStream_t)stream);
   return e == cudaSuccess ? KV_OK : api_cuda_fail(e, (who + ": launch").c_str());

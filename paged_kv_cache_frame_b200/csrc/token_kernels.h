@@ -75,7 +75,8 @@ struct DecodeArgs {
   int warps;                  // of a CTA (decode_shape.h)
   int tile_shift;             // log2 of a tile's tokens
   int part_tiles;             // tiles that are not worth a join
-  float scale_log2;           // scale * log2(e)
+  float scale_log2;           // scale * log2(e) / q_down
+  float q_down;               // power of two on a step's queries in fp16, 1 elsewhere
   RopeTable rope;
 };
 

@@ -124,3 +124,23 @@ def test_scores_that_are_all_minus_infinity(pkv, lens, hkv, g, d, dtype):
     b.len_t.zero_()
     assert bool((b.cache.decode(q) == 0).all())
     b.cache.check_device()
+
+
+@pytest.mark.parametrize("amplitude", [None, 3.0, 1e4])
+@pytest.mark.parametrize("layout,d,g", [("half", 64, 1), ("interleaved", 128, 16)])
+def test_rotated_queries_past_the_types_range(pkv, amplitude, layout, d, g):
+    """In the step a rotated query is not rounded to the pool's type: values that fp16 does not reach count as they are."""
+    b = Batch(pkv, [200, 3000], 2, d, 64, "fp16", seed=35)
+    for s, n in enumerate(b.lens):
+        p, r = b.where(s, torch.arange(n, device="cuda"))
+        b.pool[p, 0, r] *= 2**-8
+    rope = pkv.Rope(d, layout=layout, inv_freq=[0.7 + 0.01 * i for i in range(d // 2)], amplitude=amplitude)
+    q = (randn((2, 2 * g, d), b.dtype, b.g).sign() * 60000).to(b.dtype)
+    k, v = randn((2, 2, d), b.dtype, b.g) * 2**-14, randn((2, 2, d), b.dtype, b.g)
+    pos = torch.tensor([3, 70001], dtype=torch.int32, device="cuda")
+    scale = 2**-9 / (amplitude or 1)
+    out = b.cache.decode_append(k, v, q, rope=rope, positions=pos, scale=scale)
+    b.cache.check_device()
+    exact_q = torch.tensor(turned(q, pos, rope)[0], device="cuda")
+    assert float(exact_q.abs().max()) > 65504
+    assert_attended(out, b, exact_q, scale=scale, extra=2**-16 + ROT)
