@@ -140,6 +140,7 @@ struct Rotation : torch::autograd::Function<Rotation> {
     const at::Tensor positions = ctx->get_saved_variables()[0];
     at::Tensor dy = g[0];
     if (!dy.defined()) return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+    dy = dy.resolve_neg();   // a view whose values are not the memory's: not the user's to resolve
     if (dy.stride(-1) != 1) dy = dy.contiguous();
     auto rope = c10::static_intrusive_pointer_cast<Rope>(ctx->saved_data["rope"].toCapsule());
     const bool inverse = !ctx->saved_data["inverse"].toBool();

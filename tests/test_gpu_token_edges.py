@@ -144,3 +144,13 @@ def test_rotated_queries_past_the_types_range(pkv, amplitude, layout, d, g):
     exact_q = torch.tensor(turned(q, pos, rope)[0], device="cuda")
     assert float(exact_q.abs().max()) > 65504
     assert_attended(out, b, exact_q, scale=scale, extra=2**-16 + ROT)
+
+
+# ---------------------------------------------------------------- derivatives and overlaps
+def test_a_negated_gradient(pkv):
+    rope, pos = pkv.Rope(64), torch.arange(5, device="cuda", dtype=torch.int32)
+    x = torch.randn(5, 2, 64, device="cuda", requires_grad=True)
+    dy = torch.randn(5, 2, 64, device="cuda")
+    want, = torch.autograd.grad(rope.rotate(x, pos), x, -dy)
+    got, = torch.autograd.grad(rope.rotate(x, pos), x, torch._neg_view(dy))
+    assert torch.equal(got, want)
