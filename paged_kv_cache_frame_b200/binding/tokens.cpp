@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/MemoryOverlap.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -64,8 +65,15 @@ void check_device(const at::Tensor& x, const char* name) {
   TORCH_CHECK_VALUE(x.is_cuda(), name, ": must be a CUDA tensor, not on ", x.device());
 }
 
+// No operator has a forward-mode derivative: a tangent is refused, not dropped.
+void check_no_tangent(const at::Tensor& x, const char* name) {
+  TORCH_CHECK_VALUE(!x._fw_grad(0).defined() || !c10::AutogradState::get_tls_state().get_fw_grad_mode(), name,
+                    ": carries a tangent, and there is no forward-mode derivative (unpack_dual it)");
+}
+
 // The operators without a gradient refuse inputs that would want one.
 void check_no_gradient(const at::Tensor& x, const char* name) {
+  check_no_tangent(x, name);
   TORCH_CHECK_VALUE(!x.requires_grad() || !at::GradMode::is_enabled(), name,
                     ": requires a gradient, which this operator does not have (detach it or call under torch.no_grad)");
 }
@@ -108,6 +116,7 @@ at::Tensor rotate(const c10::intrusive_ptr<Rope>& rope, const at::Tensor& x, con
   const int code = dtype_code(x.scalar_type());
   TORCH_CHECK_VALUE(code >= 0, "x: dtype ", x.scalar_type(), ", expected bfloat16, float16 or float32");
   TORCH_CHECK_VALUE(x.dim() == 3, "x: shape ", shown(x.sizes()), ", expected [tokens, heads, head_dim]");
+  check_no_tangent(x, "x");
   check_device(x, "x");
   check_tensor(x, "x", x.sizes(), x.scalar_type(), x.device(), false);
   TORCH_CHECK_VALUE(x.size(0) <= INT32_MAX && x.size(1) <= INT32_MAX && x.size(2) <= INT32_MAX, "x: too large");

@@ -170,7 +170,7 @@ class Rope:
         """x [tokens, heads, head_dim] (bfloat16, float16 or float32; the
         last dimension dense) rotated at positions [tokens] (int32), into
         `out` if given (x itself, or apart from it). Differentiable in x, the
-        gradient too. A captured backward pass belongs in one capture with its
+        gradient too, in reverse mode (tangents are refused). A captured backward pass belongs in one capture with its
         forward, through torch.autograd.grad: a captured .backward() meets the
         streams of any eager graph of the same leaves that is still alive."""
         if stream is None:

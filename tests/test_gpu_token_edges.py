@@ -154,3 +154,22 @@ def test_a_negated_gradient(pkv):
     want, = torch.autograd.grad(rope.rotate(x, pos), x, -dy)
     got, = torch.autograd.grad(rope.rotate(x, pos), x, torch._neg_view(dy))
     assert torch.equal(got, want)
+
+
+def test_forward_mode_is_refused(pkv):
+    """No operator has a forward-mode derivative: a tangent is refused, not dropped."""
+    import torch.autograd.forward_ad as fwd
+    b, rope = Batch(pkv, [10, 20], 2, 64, 16, seed=36), pkv.Rope(64)
+    k, q, pos = randn((2, 2, 64), b.dtype, b.g), randn((2, 4, 64), b.dtype, b.g), b.len_t - 1
+    x = randn((2, 3, 64), torch.float32, b.g)
+    with fwd.dual_level():
+        dual = lambda y: fwd.make_dual(y, torch.ones_like(y))  # noqa: E731
+        for call in (lambda: rope.rotate(dual(x), pos), lambda: rope.rotate(x, pos, out=dual(x.clone())),
+                     lambda: b.cache.decode(dual(q)), lambda: b.cache.append(k, dual(k)),
+                     lambda: b.cache.decode_append(dual(k), k, q), lambda: b.cache.decode(q, out=dual(torch.empty_like(q)))):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        with pytest.raises((RuntimeError, ValueError)):
+            rope.rotate(dual(x.clone().requires_grad_()), pos)
+        rope.rotate(x, pos)
+        b.cache.decode(q)
