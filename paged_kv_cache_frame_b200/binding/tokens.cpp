@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "kv.h"
+#include "overlap.h"
 
 namespace {
 
@@ -94,6 +95,19 @@ kv_rows rows_of(const at::Tensor& x) {
   return {x.data_ptr(), x.size(0) > 1 ? x.stride(0) : 0, x.size(1) > 1 ? x.stride(1) : 0};
 }
 
+pkv::RowSet bytes_of(const at::Tensor& x, const kv_rows& r) {
+  const int64_t size = x.element_size();
+  return {reinterpret_cast<int64_t>(r.data), x.size(0), x.size(1), x.size(2) * size, r.token_stride * size, r.head_stride * size};
+}
+pkv::RowSet bytes_of(const at::Tensor& x) {   // contiguous
+  return {reinterpret_cast<int64_t>(x.data_ptr()), 1, 1, (int64_t)x.nbytes(), 0, 0};
+}
+
+// What a call writes lies apart from what it reads.
+void check_apart(const pkv::RowSet& x, const char* name, const pkv::RowSet& read, const char* other) {
+  TORCH_CHECK_VALUE(!pkv::share_memory(x, read), name, ": shares memory with ", other, ", which the call reads");
+}
+
 const int32_t* index_of(const c10::optional<at::Tensor>& x, const char* name, int64_t n, at::Device device) {
   if (!x) return nullptr;
   check_tensor(*x, name, {n}, at::kInt, device, true);
@@ -128,6 +142,8 @@ at::Tensor rotate(const c10::intrusive_ptr<Rope>& rope, const at::Tensor& x, con
   const c10::cuda::OptionalCUDAGuard guard(x.device());
   at::Tensor out = given ? *given : empty_rows(x);
   const kv_rows from = rows_of(x), to = rows_of(out);
+  if (given && !(from.data == to.data && from.token_stride == to.token_stride && from.head_stride == to.head_stride))
+    check_apart(bytes_of(out, to), "out", bytes_of(x, from), "x");
   check_status(kv_rotate(rope->handle, &from, &to, positions.data_ptr<int32_t>(), (int)x.size(0), (int)x.size(1),
                          (int)x.size(2), code, inverse, c10::cuda::getCurrentCUDAStream(x.device().index()).stream()),
                "kv_rotate");
@@ -204,6 +220,8 @@ void append(Tokens& t, const at::Tensor& k, const at::Tensor& v, const c10::opti
   const int32_t* pos = index_of(positions, "positions", n, t.device);
   const c10::cuda::OptionalCUDAGuard guard(t.device);
   const kv_rows kr = rows_of(k), vr = rows_of(v);
+  check_apart(bytes_of(t.pool), "pool", bytes_of(k, kr), "k");
+  check_apart(bytes_of(t.pool), "pool", bytes_of(v, vr), "v");
   check_status(kv_append_tokens(&t.c, &kr, &vr, (int)n, cu, rope ? rope->handle : nullptr, pos, stream_of(t)),
                "kv_append_tokens");
   written(t.pool);
@@ -246,8 +264,18 @@ at::Tensor decode(Tokens& t, const c10::optional<at::Tensor>& k, const c10::opti
     ws = kept;
   }
   const kv_rows qr = rows_of(q);
+  if (given) {
+    const pkv::RowSet to = bytes_of(out);
+    check_apart(to, "out", bytes_of(t.pool), "pool");
+    if (!(out.data_ptr() == qr.data && q.is_contiguous())) check_apart(to, "out", bytes_of(q, qr), "q");
+  }
   if (k) {
     const kv_rows kr = rows_of(*k), vr = rows_of(*v);
+    const pkv::RowSet kb = bytes_of(*k, kr), vb = bytes_of(*v, vr), pool = bytes_of(t.pool);
+    check_apart(pool, "pool", kb, "k");
+    check_apart(pool, "pool", vb, "v");
+    check_apart(pool, "pool", bytes_of(q, qr), "q");
+    if (given) check_apart(bytes_of(out), "out", kb, "k"), check_apart(bytes_of(out), "out", vb, "v");
     check_status(kv_decode_append(&t.c, &kr, &vr, &qr, (int)heads, rope ? rope->handle : nullptr, pos, s, (int)window,
                                   out.data_ptr(), ws.data_ptr(), ws.nbytes(), stream),
                  "kv_decode_append");

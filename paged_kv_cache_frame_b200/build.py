@@ -25,6 +25,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
 BINDING_SRC = os.path.join(HERE, "binding", "tokens.cpp")
+BINDING_DEPS = [BINDING_SRC, os.path.join(HERE, "binding", "overlap.h"), os.path.join(ROOT, "include", "kv.h")]
 BINDING = os.path.join(OUT_DIR, "_tokens.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -102,7 +103,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
 
 def build_binding(force: bool = False, verbose: bool = False) -> None:
     """Compile the binding (if stale) with g++; it links to libpkv.so beside it."""
-    if not force and not _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "kv.h")]):
+    if not force and not _stale(BINDING, BINDING_DEPS):
         return
     try:
         import torch

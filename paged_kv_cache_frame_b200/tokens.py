@@ -265,8 +265,9 @@ class PagedTokens:
     def decode(self, q, out=None, scale=None, window=0, workspace=None, stream=None):
         """Attention of one new token per sequence: q [n_seqs, q heads,
         head_dim] against the sequence's last `window` tokens (0: all). scale:
-        default 1/sqrt(head_dim). workspace: of workspace() (default: one per
-        stream, in a capture one per call, prepared by the graph)."""
+        default 1/sqrt(head_dim). out: q itself, or apart from q and the pool.
+        workspace: of workspace() (default: one per stream, in a capture one
+        per call, prepared by the graph)."""
         if stream is None:
             return _native.decode(self._native, None, None, q, None, None, out, scale, window, workspace)
         with _on(self._pool.device, stream):

@@ -173,3 +173,39 @@ def test_forward_mode_is_refused(pkv):
             rope.rotate(dual(x.clone().requires_grad_()), pos)
         rope.rotate(x, pos)
         b.cache.decode(q)
+
+
+def test_outputs_that_overlap_inputs_are_refused(pkv):
+    """`out` is x (or q) itself or apart from every input; what lies in the same memory and is neither is refused."""
+    b, rope = Batch(pkv, [10, 20], 2, 64, 16, seed=37, poison=False), pkv.Rope(64)
+    pos = b.len_t - 1
+    buf = randn((40, 64), torch.float32, b.g)
+    x, wide, flat = buf[:6].view(2, 3, 64), buf.view(2, 20, 64), buf.view(-1)
+    for a, out in ((x, buf[1:7].view(2, 3, 64)), (x, buf[5:11].view(2, 3, 64)), (x, flat[2:386].view(2, 3, 64)),
+                   (x, flat[383:767].view(2, 3, 64)), (wide[:, 2:5], wide[:, 4:7]), (wide[:, 2:5], wide[:, :3]),
+                   (wide[:, :3], x), (x, wide[:, :3]), (wide[:, :3], buf[21:27].view(2, 3, 64))):
+        with pytest.raises(ValueError, match="memory"):
+            rope.rotate(a, pos, out=out)
+    want = rope.rotate(wide[:, 2:5], pos)
+    rope.rotate(wide[:, 2:5], pos, out=wide[:, 5:8])    # other heads of the same rows
+    assert torch.equal(wide[:, 5:8], want)
+    rope.rotate(wide[:, 2:5], pos, out=buf[8:14].view(2, 3, 64))   # between the rows
+    assert torch.equal(buf[8:14].view(2, 3, 64), want)
+    assert torch.equal(rope.rotate(wide[:, 2:5], pos, out=wide[:, 2:5]), want)
+    q, k = randn((2, 4, 64), b.dtype, b.g), randn((2, 2, 64), b.dtype, b.g)
+    row, pad = b.pool.view(-1, 64), randn((30, 64), b.dtype, b.g)
+    inside = row[8:12].view(2, 2, 64)
+    for call in (lambda: b.cache.append(inside, k), lambda: b.cache.append(k, inside), lambda: b.cache.decode_append(inside, k, q),
+                 lambda: b.cache.decode_append(k, inside, q), lambda: b.cache.decode_append(k, k, row[:8].view(2, 4, 64)),
+                 lambda: b.cache.decode(q, out=row[:8].view(2, 4, 64)), lambda: b.cache.decode_append(k, k, q, out=row[:8].view(2, 4, 64)),
+                 lambda: b.cache.decode(pad[:8].view(2, 4, 64), out=pad[4:12].view(2, 4, 64)),
+                 lambda: b.cache.decode_append(pad[:4].view(2, 2, 64), k, q, out=pad[2:10].view(2, 4, 64)),
+                 lambda: b.cache.decode_append(k, pad[9:13].view(2, 2, 64), q, out=pad[2:10].view(2, 4, 64))):
+        with pytest.raises(ValueError, match="memory"):
+            call()
+    heads = pad.view(2, 15, 64)[:, :4]
+    want = b.cache.decode(heads)
+    assert torch.equal(b.cache.decode(heads, out=pad[5:13].view(2, 4, 64)), want)
+    assert torch.equal(b.cache.decode(row[8:16].view(2, 4, 64)), b.cache.decode(row[8:16].view(2, 4, 64).clone()))
+    want = b.cache.decode(q)
+    assert torch.equal(b.cache.decode(q, out=q), want)

@@ -244,6 +244,15 @@ def test_page_divisor(tmp_path):
     assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
 
 
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_overlap_rule(tmp_path):
+    exe = tmp_path / "overlap"
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(CSRC, "..", "binding"), os.path.join(HERE, "cpp", "overlap.cpp"),
+                    "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
+
+
 def find_seq(cu, n, t):
     """The kernel's search."""
     lo, hi = 0, n
