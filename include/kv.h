@@ -517,7 +517,8 @@ int kv_rotate(const kv_rope_t* rope, const kv_rows* x, const kv_rows* out, const
  * start on 16-byte boundaries.
  * Errors: KV_ERR_ARG, KV_ERR_UNSUPPORTED (head_dim must be 64 or 128),
  * KV_ERR_CUDA. A cu_new that runs backwards, or gives a sequence more tokens
- * than its length, raises the error word, and those tokens are not written. */
+ * than its length, raises the error word, and those tokens are not written;
+ * one that counts more than n_tokens raises it too. */
 int kv_append_tokens(const kv_tokens* c, const kv_rows* k, const kv_rows* v, int n_tokens, const int32_t* cu_new,
                      const kv_rope_t* rope, const int32_t* positions, void* stream);
 

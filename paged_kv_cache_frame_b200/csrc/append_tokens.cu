@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_tokens_kernel(con
   if (threadIdx.x < tokens) {
     const int i = threadIdx.x, t = first + i;
     const int32_t* cu = kept ? s_cu : a.cu_new;
+    if (cu && t == 0 && cu[n] > a.n_tokens) raise_error(a.c.error, kErrIndex);   // tokens that the call does not bring
     int s = t, back = 1;   // the token is the back-th from the end of sequence s
     if (cu) {
       s = find_seq(cu, n, t);

@@ -209,3 +209,27 @@ def test_outputs_that_overlap_inputs_are_refused(pkv):
     assert torch.equal(b.cache.decode(row[8:16].view(2, 4, 64)), b.cache.decode(row[8:16].view(2, 4, 64).clone()))
     want = b.cache.decode(q)
     assert torch.equal(b.cache.decode(q, out=q), want)
+
+
+# ---------------------------------------------------------------- appending
+def test_a_cu_new_past_the_tokens_given_is_reported(pkv):
+    """Tokens that cu_new counts and the call does not bring: those that it brings are written, the lack is reported."""
+    b = Batch(pkv, [20, 20, 20], 2, 64, 8, seed=38)
+    k, v = randn((7, 2, 64), b.dtype, b.g), randn((7, 2, 64), b.dtype, b.g)
+    for cu, ok in (([0, 3, 3, 7], True), ([0, 3, 3, 8], False), ([0, 3, 9, 9], False), ([0, 3, 7, 2000000000], False),
+                   ([0, 2, 3, 5], True)):
+        b.cache.append(k, v, cu_new=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        if ok:
+            b.cache.check_device()
+        else:
+            with pytest.raises(pkv.KVError) as e:
+                b.cache.check_device()
+            assert e.value.name == "DEVICE_CHECK"
+    many = Batch(pkv, [1] * 1500, 1, 64, 4, seed=39)   # more sequences than are searched in shared memory
+    cu = torch.arange(1501, dtype=torch.int32, device="cuda")
+    x = randn((1500, 1, 64), many.dtype, many.g)
+    many.cache.append(x, x, cu_new=cu)
+    many.cache.check_device()
+    with pytest.raises(pkv.KVError):
+        many.cache.append(x[:1499], x[:1499], cu_new=cu)
+        many.cache.check_device()
