@@ -326,6 +326,13 @@ int kv_get_page_table(const kv_plan_t* plan, int stream_idx, int* indices, int c
 int kv_get_kv_tiles(const kv_plan_t* plan, int stream_idx, int* row, int* lo, int* hi, int* krow, int* step,
                     int cap, int* n);
 
+/* kv_plan_check -- whether the tokens of stream `stream_idx`'s page table are
+ * in `block`'s pool: KV_ERR_STALE_PLAN where the stream's cache changed after
+ * kv_plan, KV_ERR_NOT_APPENDED where the block of the open step is not written
+ * yet, KV_ERR_ARG, else KV_OK. For callers that read the pool by
+ * kv_get_page_table (kv_run makes these checks itself). Host only. */
+int kv_plan_check(const kv_plan_t* plan, int stream_idx, int block);
+
 /* kv_plan_get_stats -- summary of the plan's schedule. */
 int kv_plan_get_stats(const kv_plan_t* plan, kv_plan_stats* out);
 

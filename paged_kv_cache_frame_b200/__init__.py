@@ -32,7 +32,7 @@ __all__ = [
     "kv_evict_frames", "kv_defer_eviction", "kv_commit_frame", "kv_rollback_last_frame",
     "kv_get_stats", "kv_get_config", "kv_get_free_list", "kv_workspace_bytes", "kv_plan", "kv_run",
     "kv_run_append", "kv_begin_frame", "kv_plan_free", "kv_get_page_table", "kv_get_kv_tiles",
-    "kv_plan_get_stats", "kv_check_device", "kv_testing_fail_launches", "kv_strerror",
+    "kv_plan_check", "kv_plan_get_stats", "kv_check_device", "kv_testing_fail_launches", "kv_strerror",
     "kv_last_error", "kv_run_static", "kv_set_cross_frame_special", "kv_set_camera_only",
     "Rope", "PagedTokens", "KV_FP32", "kv_rope_init", "kv_rope_init_frequencies", "kv_rope_free", "kv_rope_get",
     "kv_rotate", "kv_append_tokens", "kv_decode_workspace_bytes",
@@ -207,6 +207,10 @@ def kv_get_kv_tiles(plan, stream_idx=0, with_krow=False):
     if with_krow:
         return [(row[i], lo[i], hi[i], kr[i], sp[i]) for i in range(n.value)]
     return [(row[i], lo[i], hi[i]) for i in range(n.value)]
+
+
+def kv_plan_check(plan, stream_idx, block) -> None:
+    capi.check(capi.lib().kv_plan_check(plan, stream_idx, block), "kv_plan_check")
 
 
 def kv_plan_get_stats(plan) -> dict:

@@ -122,6 +122,7 @@ SIGNATURES = {
     "kv_get_kv_tiles": (_I, [_P, _I, _IP, _IP, _IP, _IP, _IP, _I, _IP]),
     "kv_plan_get_stats": (_I, [_P, ctypes.POINTER(kv_plan_stats)]),
     "kv_check_device": (_I, [_P, _P]),
+    "kv_plan_check": (_I, [_P, _I, _I]),
     "kv_run_static": (_I, [ctypes.POINTER(_P), _I, _I, _I, _P, _P, _I, _P]),
     "kv_set_cross_frame_special": (_I, [_P, _I]),
     "kv_set_camera_only": (_I, [_P, _I]),

@@ -563,6 +563,16 @@ int kv_get_kv_tiles(const kv_plan_t* p, int stream_idx, int* row, int* lo, int* 
   return KV_OK;
 }
 
+int kv_plan_check(const kv_plan_t* p, int stream_idx, int block) {
+  if (!p) return fail(KV_ERR_ARG, "kv_plan_check: NULL plan");
+  if (stream_idx < 0 || stream_idx >= (int)p->caches.size()) return fail(KV_ERR_ARG, "kv_plan_check: stream out of range");
+  const pkv::PageState& st = p->caches[stream_idx]->st;
+  if (block < 0 || block >= st.cfg.B) return fail(KV_ERR_ARG, "kv_plan_check: block out of range");
+  if (st.epoch != p->epochs[stream_idx]) return fail(KV_ERR_STALE_PLAN, "kv_plan_check: cache state changed after kv_plan");
+  if (st.step_open && !st.appended[block]) return fail(KV_ERR_NOT_APPENDED, "kv_plan_check: block not appended in this step");
+  return KV_OK;
+}
+
 int kv_plan_get_stats(const kv_plan_t* p, kv_plan_stats* out) {
   if (!p || !out) return fail(KV_ERR_ARG, "kv_plan_get_stats: NULL argument");
   out->n_streams = (int)p->caches.size();

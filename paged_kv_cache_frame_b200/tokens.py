@@ -211,11 +211,14 @@ class PagedTokens:
         attends to, for decode(). streams: indices into the plan's caches
         (default all), whose pools must be one (a group's, or one cache's).
         Tables and lengths are copies: they hold until a cache's page state
-        changes. Refused where pages hold tokens that the plan hides."""
+        changes. Refused where a cache changed after the plan, where the open
+        step's block is not written yet, and where pages hold tokens that the
+        plan hides."""
         _bind()
         streams = list(range(len(plan.caches))) if streams is None else list(streams)
         if not streams:
             raise ValueError("streams: none given")
+        from . import kv_get_kv_tiles, kv_plan_check
         pool = plan.caches[streams[0]].pools[block]
         if pool is None or isinstance(pool, int):
             raise ValueError("of_plan: the block's pool must be bound as a tensor")
@@ -224,9 +227,9 @@ class PagedTokens:
             c = plan.caches[i]
             if c.pools[block] is not pool:
                 raise ValueError("streams: their caches do not share one pool")
+            kv_plan_check(plan.handle, i, block)
             pages, last = plan.page_table(i)
             n = (len(pages) - 1) * c.page_size + last
-            from . import kv_get_kv_tiles
             if sum(-(-(hi - lo) // step) for _, lo, hi, _, step in kv_get_kv_tiles(plan.handle, i, True)) != n:
                 raise ValueError(f"streams: stream {i}'s pages hold tokens that the plan hides")
             tables.append(pages)

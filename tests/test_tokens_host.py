@@ -234,6 +234,53 @@ def test_counts_and_scales_at_the_edge_of_their_types(pkv):
         assert code(pkv, pkv.kv_decode_append, c, x, x, x, 2, None, None, scale, 0, 4096, 4096, big) == "ARG"
 
 
+# ---------------------------------------------------------------- frame plans
+def test_plans_whose_tables_do_not_hold_are_refused(pkv):
+    """kv_plan_check and PagedTokens.of_plan take a plan where its tokens are in the pool, stream by stream and block by block."""
+    import torch
+    caches = pkv.PagedKVCache.group(2, 40, 16, 2, 64, scale_frames=1, window=2, num_special=4, num_blocks=2)
+    caches[0].pools[:] = [torch.zeros(40, 2, 16, 2, 64, dtype=torch.bfloat16)] * 2   # stand-ins: no call reaches them
+
+    def frame(c, blocks=(0, 1)):
+        for b in blocks:
+            c.append_frame(b, None, None)
+        c.evict_frames()
+
+    def of_plan(plan, block, streams=None):   # refused for its state (KVError), or only then for not being on a GPU
+        try:
+            pkv.PagedTokens.of_plan(plan, block, streams)
+        except pkv.KVError as e:
+            return e.name
+        except ValueError as e:
+            assert "CUDA" in str(e)
+            return "OK"
+
+    for _ in range(4):
+        frame(caches[0])
+        frame(caches[1])
+    plan = pkv.Plan(caches)
+    assert [of_plan(plan, b) for b in (0, 1)] == ["OK", "OK"]
+    frame(caches[1])                                    # its oldest page is another frame's by then
+    assert of_plan(plan, 0) == of_plan(plan, 0, [1]) == "STALE_PLAN" and of_plan(plan, 0, [0]) == "OK"
+    pkv.kv_plan_check(plan.handle, 0, 1)
+    assert code(pkv, pkv.kv_plan_check, plan.handle, 1, 0) == "STALE_PLAN"
+    caches[0].begin_frame()                             # a step's pages are taken, its blocks not written
+    plan = pkv.Plan(caches)
+    assert of_plan(plan, 0) == of_plan(plan, 1, [0]) == "NOT_APPENDED" and of_plan(plan, 0, [1]) == "OK"
+    caches[0].append_frame(0, None, None)
+    assert of_plan(plan, 0) == "OK" and of_plan(plan, 1) == "NOT_APPENDED"
+    caches[0].append_frame(1, None, None)
+    assert of_plan(plan, 1) == "OK"
+    caches[1].defer_eviction()
+    frame(caches[1])
+    caches[1].rollback_last_frame()                     # what is left is written, with no step open
+    assert of_plan(plan, 1, [1]) == "STALE_PLAN" and of_plan(pkv.Plan(caches), 1) == "OK"
+    caches[1].reset()
+    assert of_plan(plan, 1, [1]) == "STALE_PLAN"
+    for args in ((None, 0, 0), (plan.handle, 2, 0), (plan.handle, -1, 0), (plan.handle, 0, 2), (plan.handle, 0, -1)):
+        assert code(pkv, pkv.kv_plan_check, *args) == "ARG"
+
+
 # ---------------------------------------------------------------- index arithmetic
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_page_divisor(tmp_path):
