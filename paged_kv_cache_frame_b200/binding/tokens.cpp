@@ -179,6 +179,7 @@ struct Rotation : torch::autograd::Function<Rotation> {
 struct Tokens {
   kv_tokens c;
   at::Tensor pool, tables, lens, error;   // what `c` points to
+  bool read_only;                         // the pages belong to frame caches
   at::ScalarType dtype;
   at::Device device;
   std::map<std::pair<void*, int64_t>, at::Tensor> workspaces;   // of eager calls, by stream and query heads
@@ -203,6 +204,7 @@ at::Tensor new_workspace(Tokens& t, int64_t heads) {
 
 // k and v [n, heads, head_dim] of new tokens.
 void check_new(const Tokens& t, const at::Tensor& k, const at::Tensor& v, int64_t n) {
+  TORCH_CHECK_VALUE(!t.read_only, "the tokens of a frame plan are read only: their pages and slots are the caches'");
   const int64_t shape[] = {n, t.c.num_heads, t.c.head_dim};
   check_tensor(k, "k", shape, t.dtype, t.device, false);
   check_tensor(v, "v", shape, t.dtype, t.device, false);
@@ -375,8 +377,8 @@ PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (rope, x
   });
 }
 
-PyObject* py_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (pool, tables, lens)
-  if (n != 3) return expect(n, 3);
+PyObject* py_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (pool, tables, lens, read_only)
+  if (n != 4) return expect(n, 4);
   return guarded([&]() -> PyObject* {
     const at::Tensor& pool = tensor(a[0], "pool");
     TORCH_CHECK_VALUE(pool.dim() == 5 && pool.size(1) == 2, "pool: shape ", shown(pool.sizes()),
@@ -392,6 +394,8 @@ PyObject* py_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (pool, t
     check_tensor(lens, "lens", {seqs}, at::kInt, pool.device(), true);
     for (int64_t s : {pool.size(0), pool.size(2), pool.size(3), pool.size(4), seqs, width})
       TORCH_CHECK_VALUE(s <= INT32_MAX, "pool, tables: too large");
+    const int read_only = PyObject_IsTrue(a[3]);
+    if (read_only < 0) throw python_error();
     const c10::cuda::OptionalCUDAGuard guard(pool.device());
     at::Tensor error = at::zeros({1}, at::TensorOptions().dtype(at::kInt).device(pool.device()));
     kv_tokens c;
@@ -407,7 +411,7 @@ PyObject* py_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {   // (pool, t
     c.dtype = dtype_code(pool.scalar_type());
     c.table_width = (int)width;
     c.n_seqs = (int)seqs;
-    auto* t = new Tokens{c, pool, tables, lens, error, pool.scalar_type(), pool.device(), {}, {}};
+    auto* t = new Tokens{c, pool, tables, lens, error, read_only != 0, pool.scalar_type(), pool.device(), {}, {}};
     return PyCapsule_New(t, kTokensName,
                          [](PyObject* o) { delete static_cast<Tokens*>(PyCapsule_GetPointer(o, kTokensName)); });
   });

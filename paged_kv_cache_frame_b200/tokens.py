@@ -192,9 +192,9 @@ class PagedTokens:
     as long as a captured call may be replayed, and order its use on another
     stream behind its construction, as for any tensor."""
 
-    def __init__(self, pool, tables, lens):
+    def __init__(self, pool, tables, lens, _read_only=False):
         _bind()
-        self._native = _native.tokens(pool, tables, lens)
+        self._native = _native.tokens(pool, tables, lens, _read_only)
         self._pool, self._tables, self._lens = pool, tables, lens
         self._c = capi.kv_tokens.from_address(_native.address(self._native))   # for the C names
         self.n_seqs = tables.shape[0]
@@ -208,7 +208,8 @@ class PagedTokens:
     @classmethod
     def of_plan(cls, plan, block, streams=None):
         """The tokens that a frame plan shows, as sequences: what kv_run
-        attends to, for decode(). streams: indices into the plan's caches
+        attends to, for decode(). Read only: append() and decode_append() are
+        refused, as the pages and their free slots are the caches'. streams: indices into the plan's caches
         (default all), whose pools must be one (a group's, or one cache's).
         Tables and lengths are copies: they hold until a cache's page state
         changes. Refused where a cache changed after the plan, where the open
@@ -239,7 +240,7 @@ class PagedTokens:
         shape = (c.max_pages, 2, c.page_size, c.H, c.D)
         return cls(pool.view(-1)[:c.max_pages * 2 * c.page_size * c.H * c.D].view(shape),
                    torch.tensor([t + [0] * (width - len(t)) for t in tables], dtype=torch.int32, device=pool.device),
-                   torch.tensor(lens, dtype=torch.int32, device=pool.device))
+                   torch.tensor(lens, dtype=torch.int32, device=pool.device), _read_only=True)
 
     def append(self, k, v, cu_new=None, rope=None, positions=None, stream=None):
         """Write new tokens' k and v [tokens, heads, head_dim], the keys

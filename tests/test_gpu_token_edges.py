@@ -233,3 +233,36 @@ def test_a_cu_new_past_the_tokens_given_is_reported(pkv):
     with pytest.raises(pkv.KVError):
         many.cache.append(x[:1499], x[:1499], cu_new=cu)
         many.cache.check_device()
+
+
+# ---------------------------------------------------------------- frame plans
+def frames(pkv, n, ps=16, streams=1, **kw):
+    caches = pkv.PagedKVCache.group(streams, 40 * streams, ps, 2, 64, scale_frames=1, window=3, num_special=4, **kw)
+    caches[0].allocate_pools("cuda")
+    g = gen(40)
+    for _ in range(n):
+        for c in caches:
+            for block in range(c.num_blocks):
+                x = randn((2, ps + 4, 2, 64), DT[c.dtype], g)
+                c.append_frame(block, x[0], x[1])
+            c.evict_frames()
+    return caches
+
+
+def test_tokens_of_a_plan_are_read_only(pkv):
+    """The pages are the caches': a token has no slot of its own there."""
+    caches = frames(pkv, 6, streams=2)
+    seqs = pkv.PagedTokens.of_plan(pkv.Plan(caches), 0)
+    before = caches[0].pools[0].clone()
+    q = torch.ones((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    want = seqs.decode(q)
+    for _ in range(2):
+        for call in (lambda: seqs.append(q, q), lambda: seqs.decode_append(q, q, q),
+                     lambda: seqs.append(q, q, cu_new=torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"))):
+            with pytest.raises(ValueError, match="read"):
+                call()
+        seqs.lens.add_(1)
+    assert torch.equal(bits(caches[0].pools[0]), bits(before))
+    seqs.lens.sub_(2)
+    assert torch.equal(seqs.decode(q), want)
+    seqs.check_device()
