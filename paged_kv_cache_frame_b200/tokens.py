@@ -219,7 +219,7 @@ class PagedTokens:
         streams = list(range(len(plan.caches))) if streams is None else list(streams)
         if not streams:
             raise ValueError("streams: none given")
-        from . import kv_get_kv_tiles, kv_plan_check
+        from . import _torch_dtype, kv_get_kv_tiles, kv_plan_check
         pool = plan.caches[streams[0]].pools[block]
         if pool is None or isinstance(pool, int):
             raise ValueError("of_plan: the block's pool must be bound as a tensor")
@@ -238,7 +238,8 @@ class PagedTokens:
         width = max(len(t) for t in tables)
         c = plan.caches[streams[0]]
         shape = (c.max_pages, 2, c.page_size, c.H, c.D)
-        return cls(pool.view(-1)[:c.max_pages * 2 * c.page_size * c.H * c.D].view(shape),
+        # the cache's bytes in the cache's type: bind_pool takes any tensor that is large enough
+        return cls(pool.view(-1).view(torch.uint8)[:c.pool_bytes()].view(_torch_dtype(c.fp16)).view(shape),
                    torch.tensor([t + [0] * (width - len(t)) for t in tables], dtype=torch.int32, device=pool.device),
                    torch.tensor(lens, dtype=torch.int32, device=pool.device), _read_only=True)
 

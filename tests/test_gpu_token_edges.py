@@ -266,3 +266,14 @@ def test_tokens_of_a_plan_are_read_only(pkv):
     seqs.lens.sub_(2)
     assert torch.equal(seqs.decode(q), want)
     seqs.check_device()
+
+
+def test_a_plans_pool_is_read_in_the_caches_type(pkv):
+    """bind_pool takes any tensor of enough bytes: the cache's dtype is what its values are."""
+    caches = frames(pkv, 4, dtype="fp16")
+    q = randn((1, 2, 64), torch.float16, gen(41))
+    want = pkv.PagedTokens.of_plan(pkv.Plan(caches), 0).decode(q)
+    pool = caches[0].pools[0]
+    for other in (pool.view(torch.bfloat16), pool.view(torch.uint8), pool.view(-1).view(torch.float32)):
+        caches[0].pools[0] = other
+        assert torch.equal(pkv.PagedTokens.of_plan(pkv.Plan(caches), 0).decode(q), want)
