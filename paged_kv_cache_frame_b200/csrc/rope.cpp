@@ -56,7 +56,8 @@ int rope_frequencies(const RopeSpec& s, double* theta, double* amplitude, std::s
 int rope_table(int rot_dim, int layout, const double* theta, double amplitude, RopeTable* out, std::string* why) {
   const int rc = check_shape(rot_dim, layout, why);
   if (rc != KV_OK) return rc;
-  if (!std::isfinite(amplitude) || amplitude <= 0) return bad(why, "rope: amplitude must be positive");
+  if (!std::isfinite((float)amplitude) || (float)amplitude <= 0)   // the kernels' own
+    return bad(why, "rope: amplitude must be positive, and fit 32 bits");
   std::memset(out, 0, sizeof(*out));
   for (int i = 0; i < rot_dim / 2; ++i) {
     // Up to 64 the quotient's 64-bit mantissa leaves its fraction within

@@ -72,6 +72,13 @@ def test_rope_refusals(pkv, kw):
     assert code(pkv, lambda: pkv.Rope(**kw)) == "ARG"
 
 
+@pytest.mark.parametrize("amplitude", [1e300, 3.5e38, 1e-60, 1e-46])
+def test_amplitudes_that_do_not_fit_32_bits_are_refused(pkv, amplitude):
+    """The kernels' factor would be infinite, or 0."""
+    assert code(pkv, lambda: pkv.Rope(8, amplitude=amplitude)) == "ARG"
+    assert code(pkv, lambda: pkv.Rope(4, inv_freq=[1.0, 0.5], amplitude=amplitude)) == "ARG"
+
+
 @pytest.mark.parametrize("kw", [
     {"rot_dim": 4, "layout": "thirds"}, {"rot_dim": 4, "scaling": "cubic"}, {"rot_dim": 4, "amplitude": 0.0},
     {"rot_dim": 4, "amplitude": math.nan}, {"rot_dim": 4, "inv_freq": [1.0]},
