@@ -13,6 +13,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -27,6 +28,7 @@ LIB = os.path.join(OUT_DIR, "libpkv.so")
 BINDING_SRC = os.path.join(HERE, "binding", "tokens.cpp")
 BINDING_DEPS = [BINDING_SRC, os.path.join(HERE, "binding", "overlap.h"), os.path.join(ROOT, "include", "kv.h")]
 BINDING = os.path.join(OUT_DIR, "_tokens.so")
+BINDING_MADE_FOR = os.path.join(OBJ_DIR, "_tokens.for")   # the torch and Python that it was compiled against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -101,9 +103,26 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     return LIB
 
 
+def _torch_and_python() -> str:
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "no torch"
+    return f"{torch} {sys.implementation.cache_tag}"
+
+
+def binding_stale() -> bool:
+    """Compiled from other sources, or against another torch or Python: their
+    C++ interfaces are not the same."""
+    if _stale(BINDING, BINDING_DEPS) or not os.path.exists(BINDING_MADE_FOR):
+        return True
+    with open(BINDING_MADE_FOR) as f:
+        return f.read() != _torch_and_python()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> None:
     """Compile the binding (if stale) with g++; it links to libpkv.so beside it."""
-    if not force and not _stale(BINDING, BINDING_DEPS):
+    if not force and not binding_stale():
         return
     try:
         import torch
@@ -125,6 +144,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_MADE_FOR, "w") as f:
+        f.write(_torch_and_python())
 
 
 def main():

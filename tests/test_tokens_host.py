@@ -288,6 +288,18 @@ def test_plans_whose_tables_do_not_hold_are_refused(pkv):
         assert code(pkv, pkv.kv_plan_check, *args) == "ARG"
 
 
+# ---------------------------------------------------------------- the binding's build
+def test_the_binding_is_built_again_for_another_torch(pkv, monkeypatch, tmp_path):
+    from paged_kv_cache_frame_b200 import build
+    assert not build.binding_stale()
+    for name, was in (("version", "1.0"), ("none", None)):
+        at = tmp_path / name
+        if was is not None:
+            at.write_text(f"{was} {build._torch_and_python().split()[-1]}")
+        monkeypatch.setattr(build, "BINDING_MADE_FOR", str(at))
+        assert build.binding_stale()
+
+
 # ---------------------------------------------------------------- index arithmetic
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_page_divisor(tmp_path):
