@@ -277,3 +277,25 @@ def test_a_plans_pool_is_read_in_the_caches_type(pkv):
     for other in (pool.view(torch.bfloat16), pool.view(torch.uint8), pool.view(-1).view(torch.float32)):
         caches[0].pools[0] = other
         assert torch.equal(pkv.PagedTokens.of_plan(pkv.Plan(caches), 0).decode(q), want)
+
+
+# ---------------------------------------------------------------- parts of four-warp launches
+@pytest.mark.parametrize("n", [60000, 250000])
+@pytest.mark.parametrize("d,g,fused", [(64, 1, False), (128, 8, False), (64, 11, False), (128, 16, False), (64, 2, True), (128, 9, True)])
+def test_one_long_sequence_among_short_ones(pkv, n, d, g, fused):
+    """As many sequences as launches of four-warp CTAs take, one of them in more parts than are joined at once: the
+    sequences cut into parts where these suffice, else cut anywhere along the line."""
+    lens = [1 + i % 5 for i in range(80)]
+    lens[17] = n
+    lens[3] = 0
+    b = Batch(pkv, lens, 1, d, 500, seed=42 + g, dtype="bf16" if d == 64 else "fp16")
+    q = randn((80, g, d), b.dtype, b.g)
+    call = lambda: b.cache.decode(q, scale=0.3)  # noqa: E731
+    if fused:
+        k, v = randn((80, 1, d), b.dtype, b.g), randn((80, 1, d), b.dtype, b.g)
+        call = lambda: b.cache.decode_append(k, v, q, scale=0.3)  # noqa: E731
+    out = call()
+    assert_attended(out, b, q, scale=0.3, extra=2**-16 if fused else 0.0)
+    for _ in range(5):
+        assert torch.equal(out, call())
+    b.cache.check_device()
