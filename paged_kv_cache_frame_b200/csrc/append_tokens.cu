@@ -24,18 +24,6 @@ constexpr int kCtasPerSm = 8;
 constexpr int kAhead = 2;         // rows in flight per thread, keys and values
 constexpr int kMaxTokens = 16;    // tokens of a block
 constexpr int kMaxSeqs = 1024;    // sequences whose cu_new and lengths are kept in shared memory
-
-// Sequences of [0, n) that end at or before token t, all before the others:
-// the sequence of token t (n where no sequence holds it).
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
-  int lo = 0, hi = n;   // the answer lies in [lo, hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (cu[mid + 1] <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
 }  // namespace
 
 template <typename T, int V, bool kInter>

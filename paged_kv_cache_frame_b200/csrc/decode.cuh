@@ -64,7 +64,7 @@
 #include <float.h>
 #include <limits.h>
 
-#include "decode_shape.h"
+#include "decode_split.h"
 #include "launch.cuh"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -84,8 +84,6 @@ constexpr float kSlack = kIsFp16<T> ? 2.f : 8.f;
 // The maximum of tokens whose scores are all -inf, where that of no token is
 // -inf: their sum is 0 as well, but their softmax has no value.
 constexpr float kLowest = -FLT_MAX;
-constexpr int kJoin = 32;    // parts that one CTA joins at once (a lane each)
-constexpr int kGroup = 16;   // parts joined in a first round where there are more
 
 template <int D, int NT, bool kFused, int W>
 struct Shape {
@@ -116,14 +114,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// The first token that the query of a sequence of `len` sees, and its tiles.
-__device__ __forceinline__ int first_seen(const DecodeArgs& a, int len) {
-  return a.window > 0 && len > a.window ? len - a.window : 0;
-}
-__device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, int len) {
-  return ((uint32_t)(len - first_seen(a, len)) + (1u << a.tile_shift) - 1) >> a.tile_shift;
-}
 
 // Shared memory behind the rings. A piece's queries (as they come, and
 // rotated) take the place of the warps' O: never at once.
@@ -169,81 +159,6 @@ __device__ __forceinline__ bool rope_pair(const RopeTable& t, int p, int& e0, in
   return on;
 }
 
-// How the tiles are split over the ranks (above), and what is left of this
-// one's part. The host chooses tiles coarse enough for 31 bits.
-struct Split {
-  bool by_parts;      // a part a rank; else the line
-  uint32_t each, more;   // the line: ranks below `more` take each + 1 places, the others `each`
-  uint32_t t, end;    // places [t, end) of the line (or parts of all sequences) are left
-  // Where place t lies: place `at` of the sequence's `size`.
-  int seq;
-  uint32_t at, size, tiles;
-  int raw, later;     // the lengths of seq and seq + 1 as they stand: read a sequence ahead, as a load
-                      // takes about a microsecond while the memory is busy
-
-  __device__ __forceinline__ uint32_t rank_of(uint32_t place) const {
-    const uint32_t lower = more * (each + 1);
-    return place < lower ? place / (each + 1) : more + (place - lower) / each;
-  }
-};
-
-// The tokens of one sequence that the CTA takes.
-struct Piece {
-  int seq, raw;       // and the sequence's length as it stands: past the table's end there is no new token
-  int tok0, tok1;     // tokens [tok0, tok1)
-  int r0, parts;      // the sequence's first rank, and in how many it lies
-};
-
-__device__ __forceinline__ int raw_len(const DecodeArgs& a, int s) {
-  return s < a.c.n_seqs ? __ldg(a.c.lens + s) : 0;
-}
-__device__ __forceinline__ uint32_t parts_of(const DecodeArgs& a, uint32_t tiles) {
-  return (tiles + a.part_tiles - 1) / a.part_tiles;
-}
-
-// On to the next sequence's places.
-__device__ __forceinline__ void next_sequence(const DecodeArgs& a, Split& l) {
-  ++l.seq;
-  l.raw = l.later;
-  l.later = raw_len(a, l.seq + 1);
-  l.tiles = tiles_of(a, held(a.c, l.raw));
-  l.size = l.by_parts ? parts_of(a, l.tiles) : l.tiles ? l.tiles + kSeqCost : 0;
-  l.at = 0;
-}
-
-__device__ __forceinline__ bool next_piece(const DecodeArgs& a, uint32_t rank, Split& l, Piece& p) {
-  while (l.t < l.end) {
-    while (l.at >= l.size && l.seq < a.c.n_seqs) next_sequence(a, l);
-    if (l.seq >= a.c.n_seqs) return false;   // cannot be, unless the lengths change under the launch
-    uint32_t tile0, tile1;
-    if (l.by_parts) {
-      tile0 = l.tiles * l.at / l.size;   // tiles <= part_tiles * ranks here
-      tile1 = l.tiles * (l.at + 1) / l.size;
-      p.r0 = l.t - l.at;
-      p.parts = l.size;
-      ++l.t;
-      ++l.at;
-    } else {
-      const uint32_t n = min(l.end - l.t, l.size - l.at);
-      const uint32_t first = l.t - l.at;   // the sequence's first place; its tiles begin kSeqCost later
-      tile0 = l.at > kSeqCost ? l.at - kSeqCost : 0;
-      tile1 = l.at + n > kSeqCost ? l.at + n - kSeqCost : 0;
-      p.r0 = tile0 == 0 ? rank : l.rank_of(first + kSeqCost);
-      p.parts = (tile1 == l.tiles ? rank : l.rank_of(first + l.size - 1)) - p.r0 + 1;
-      l.t += n;
-      l.at += n;
-    }
-    if (tile0 == tile1) continue;
-    p.seq = l.seq;
-    p.raw = l.raw;
-    const int len = held(a.c, l.raw), seen = first_seen(a, len);
-    p.tok0 = seen + (int)(tile0 << a.tile_shift);
-    p.tok1 = tile1 == l.tiles ? len : seen + (int)(tile1 << a.tile_shift);
-    return true;
-  }
-  return false;
-}
-
 // The rank's part of the split. Each warp works it out by itself, a lane for a
 // stretch of the sequences.
 __device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t rank) {
@@ -262,39 +177,15 @@ __device__ __forceinline__ Split split(const DecodeArgs& a, uint32_t rank) {
     if (lane >= d) upto += o;
   }
   const unsigned long long total = __shfl_sync(0xffffffffu, upto, 31);
-  const uint32_t parts = (uint32_t)(total >> 32), places = (uint32_t)total;
   Split l;
-  l.by_parts = parts <= (uint32_t)a.ranks;
-  if (l.by_parts) {
-    l.t = min(rank, parts);
-    l.end = min(rank + 1, parts);
-    l.each = l.more = 0;
-  } else {   // more places than ranks
-    l.each = places / a.ranks;
-    l.more = places - l.each * a.ranks;
-    l.t = rank * l.each + min(rank, l.more);
-    l.end = l.t + l.each + (rank < l.more ? 1 : 0);
-  }
+  split_range(a, rank, (uint32_t)(total >> 32), (uint32_t)total, l);
   const uint32_t last = l.by_parts ? (uint32_t)(upto >> 32) : (uint32_t)upto;
   const uint32_t size = l.by_parts ? (uint32_t)(mine >> 32) : (uint32_t)mine;
   const uint32_t here = __ballot_sync(0xffffffffu, l.t < last && l.t >= last - size);
   const int owner = here ? __ffs(here) - 1 : 31;
-  l.seq = __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner) - 1;
-  uint32_t base = __shfl_sync(0xffffffffu, last - size, owner);   // the stretch's first place
-  l.later = raw_len(a, l.seq + 1);
-  for (;;) {   // to the sequence of place t within the stretch
-    next_sequence(a, l);
-    if (l.seq >= a.c.n_seqs || l.t - base < l.size) break;
-    base += l.size;
-  }
-  l.at = l.t - base;
+  // the stretch of place t: the sequence in front of it, and its first place
+  seek(a, l, __shfl_sync(0xffffffffu, here ? s0 : a.c.n_seqs, owner) - 1, __shfl_sync(0xffffffffu, last - size, owner));
   return l;
-}
-
-// Part p of a sequence that rank r0 begins: the slot of the workspace of that
-// CTA, its second if it begins the sequence, else its first.
-__device__ __forceinline__ long long part_slot(const DecodeArgs& a, int r0, int p, uint32_t unit) {
-  return 2LL * ((long long)(r0 + p) * a.units + unit) + (p == 0 ? 1 : 0);
 }
 
 // What an output is divided by, inverted: without a token seen (a sequence of
@@ -842,25 +733,22 @@ __global__ void __launch_bounds__(Shape<D, NT, kFused, W>::kThreads, Shape<D, NT
     if (!whole) {
       // The sequence's parts, this CTA's among them; the last to arrive joins.
       T* to = out + ((long long)p.seq * q_heads + q0) * D;
-      const bool two = p.parts > kJoin;
-      const int me = rank - p.r0, g0 = two ? me / kGroup * kGroup : 0;
-      const int of = two ? min(kGroup, p.parts - g0) : p.parts;
-      const int groups = (p.parts + kGroup - 1) / kGroup;
+      const Join j = join_of(rank - p.r0, p.parts);
       __syncthreads();
       if (tid == 0) {
         const bool ready = magic == kWorkspaceMagic;
         if (!ready) raise_error(a.c.error, kErrWorkspace);
-        s_last = ready && arrive_last(a.counters + part_slot(a, p.r0, g0, unit), of);
+        s_last = ready && arrive_last(a.counters + first_counter(a, p.r0, j, unit), j.of);
       }
       __syncthreads();
       bool last = s_last;
-      if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, g0, 1, of, heads, two ? nullptr : to);
-      if (last && two) {
+      if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, j.g0, 1, j.of, heads, j.two ? nullptr : to);
+      if (last && j.two) {
         __syncthreads();
-        if (tid == 0) s_last = arrive_last(a.counters + 2 * gridDim.x + part_slot(a, p.r0, 0, unit), groups);
+        if (tid == 0) s_last = arrive_last(a.counters + second_counter(a, p.r0, unit), j.groups);
         __syncthreads();
         last = s_last;
-        if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, 0, kGroup, groups, heads, to);
+        if (last) join_parts<D, T, kRows, W>(a, wo, p.r0, unit, 0, kGroup, j.groups, heads, to);
       }
     }
     if (!s_more) break;

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "host_device.h"
 #include "sm100.cuh"
 #include "token_kernels.h"
 
@@ -87,10 +88,6 @@ constexpr uint32_t kErrWorkspace = 4u;   // a workspace that was not prepared
 __device__ __forceinline__ void raise_error(uint32_t* word, uint32_t bit) { atomicOr(word, bit); }
 
 // The length of sequence s, held to what its table can name.
-__device__ __forceinline__ int held(const TokenCache& c, int n) {
-  const int most = c.table_width * c.page_size;   // <= 2^30, checked by the host
-  return n < 0 ? 0 : n > most ? most : n;
-}
 __device__ __forceinline__ int seq_len(const TokenCache& c, int s) { return held(c, __ldg(c.lens + s)); }
 __device__ __forceinline__ bool seq_len_bad(const TokenCache& c, int s) {
   const int n = __ldg(c.lens + s);
@@ -109,9 +106,6 @@ __device__ __forceinline__ int page_of(const TokenCache& c, int j) { return divi
 __device__ __forceinline__ int row_in(const TokenCache& c, int page, int j) {
   if ((unsigned)page >= (unsigned)c.max_pages) return -1;
   return page * 2 * c.page_size + (j - page_of(c, j) * c.page_size);
-}
-__device__ __forceinline__ int token_row(const TokenCache& c, int s, int j) {
-  return row_in(c, __ldg(c.tables + s * c.table_stride + page_of(c, j)), j);
 }
 
 // Head h of token row `row`: offset in elements.

@@ -311,10 +311,10 @@ def test_page_divisor(tmp_path):
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
-def test_overlap_rule(tmp_path):
-    exe = tmp_path / "overlap"
-    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(CSRC, "..", "binding"), os.path.join(HERE, "cpp", "overlap.cpp"),
-                    "-o", str(exe)], check=True)
+@pytest.mark.parametrize("name,headers", [("overlap", os.path.join(CSRC, "..", "binding")), ("decode_split", CSRC)])
+def test_rules_that_the_kernels_and_the_binding_use(tmp_path, name, headers):
+    exe = tmp_path / name
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", headers, os.path.join(HERE, "cpp", name + ".cpp"), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
 
