@@ -431,9 +431,13 @@ int kv_run_static(kv_cache_t* const* caches, int n_streams, int block, int tiles
  *                   original_context * theta_i / 2 pi, lie between low_turns
  *                   and high_turns; amplitude 0.1 ln(factor) + 1
  * (Peng et al., "YaRN: Efficient Context Window Extension of Large Language
- * Models".) Angles are reduced modulo a turn without loss, to within 2^-30 of
- * a turn, for every 32-bit position, negative ones included. Frequencies are
- * at most 64 radians a position.
+ * Models", whose text makes the share linear in the turns. Published
+ * checkpoints are commonly run with a share linear in the pair's index between
+ * two rounded bounds, which differs by tens of per cent in the middle
+ * frequencies: give theirs to kv_rope_init_frequencies, with the amplitude.)
+ * Angles are reduced modulo a turn without loss, to within 2^-30 of a turn, for
+ * every 32-bit position, negative ones included. Frequencies are at most 64
+ * radians a position.
  *
  * Paged sequences. Token j of sequence s is row j % page_size of page
  * tables[s][j / page_size]. Tables and lengths are device arrays that the

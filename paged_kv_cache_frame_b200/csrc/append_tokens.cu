@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_tokens_kernel(con
 template <typename T, int V, bool kInter>
 static cudaError_t launch(const AppendTokensArgs& a, cudaStream_t stream) {
   const int units = a.c.D / (2 * V);
-  int per_block = (a.n_tokens + 148 * kCtasPerSm - 1) / (148 * kCtasPerSm);   // all blocks at once
+  int per_block = (a.n_tokens + kSms * kCtasPerSm - 1) / (kSms * kCtasPerSm);   // all blocks at once
   if (per_block > kMaxTokens) per_block = kMaxTokens;
   const int blocks = (a.n_tokens + per_block - 1) / per_block;
   return launch_pdl(append_tokens_kernel<T, V, kInter>, dim3(blocks), dim3(kThreads),

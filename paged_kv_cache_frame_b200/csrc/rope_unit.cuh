@@ -82,11 +82,13 @@ struct RopeUnit {
   }
 };
 
+constexpr int kSms = 148;   // of a B200: sizes of blocks count on them, results do not
+
 // Tokens a block takes: enough heads per thread to hide the angles, as long
 // as every SM still gets two blocks.
 inline int rope_tokens_per_block(int n_tokens, int heads, int units, int threads, int most) {
   int n = 1;
-  while (2 * n <= most && 2LL * n * heads * units <= 8LL * threads && n_tokens / (2 * n) >= 2 * 148) n *= 2;
+  while (2 * n <= most && 2LL * n * heads * units <= 8LL * threads && n_tokens / (2 * n) >= 2 * kSms) n *= 2;
   return n;
 }
 

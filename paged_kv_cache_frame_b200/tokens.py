@@ -141,8 +141,10 @@ class Rope:
 
     layout: "half" (pairs (i, i + rot_dim / 2)) or "interleaved" (neighbours).
     scaling: "none", "linear", "ntk" or "yarn" (with original_context,
-    low_turns, high_turns). inv_freq: rot_dim / 2 frequencies in radians a
-    position in place of base and scaling. amplitude: factor on the rotated
+    low_turns, high_turns; the ramp is linear in a pair's turns over
+    original_context, so a checkpoint whose ramp is linear in the pair's index
+    needs inv_freq). inv_freq: rot_dim / 2 frequencies in radians a position
+    in place of base and scaling. amplitude: factor on the rotated
     values (default: the scaling's own)."""
 
     def __init__(self, rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_context=0,
